@@ -14,8 +14,13 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", name)
-        for name in ("fp4idx.cu", "fp4idx_stream.cu", "fp4idx_scorer.cu", "fp4idx_host.cu")]
-HDRS = [os.path.join(ROOT, "include", "fp4idx.h"), os.path.join(PKG, "csrc", "fp4idx_common.cuh")]
+        for name in ("fp4idx.cu", "fp4idx_stream.cu", "fp4idx_scorer.cu", "fp4idx_host.cu",
+                     "fp4idx_kvcache.cu", "fp4idx_topk.cu", "fp4idx_attn.cu",
+                     "fp4idx_attn_rows.cu")]
+HDRS = [*(os.path.join(ROOT, "include", name) for name in ("fp4idx.h", "fp4idx_attention.h")),
+        *(os.path.join(PKG, "csrc", name) for name in ("fp4idx_common.cuh",
+                                                       "fp4idx_attention_common.cuh",
+                                                       "fp4idx_attn.cuh"))]
 LIB = os.path.join(PKG, "libfp4idx.so")
 
 # Bit-exact fp32: no FMA contraction, IEEE division/sqrt, subnormals kept.

@@ -1,0 +1,49 @@
+// fp4idx_attn.cuh -- what the entry points of the attention operators
+// (fp4idx_attn.cu) and their kernels share.
+#pragma once
+
+#include "fp4idx_attention_common.cuh"
+
+namespace fp4idx_impl {
+
+constexpr int kMaxGrid = 152;  // persistent CTAs: one per SM
+
+// The arguments of the attention kernels.  Dense: `batch` sequences.  Sparse:
+// `batch` query tokens, each an item list of its own.
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t q_ts, q_hs;
+  int32_t half;  // fp16 elements (else bf16)
+  const uint8_t *kc, *vc;
+  const float *ks, *vs;
+  int64_t num_blocks, cstride, sstride;
+  const int32_t* table;
+  int64_t tstride;
+  // dense
+  const int32_t* ctx;
+  const int32_t* starts;
+  int32_t max_q, max_context, window, sinks;
+  // sparse
+  const int32_t* seq_ids;
+  const int32_t* indices;
+  int64_t idx_stride;
+  int32_t nsel, table_pages, num_seqs, per_seq;
+
+  int32_t batch, T, Hq, Hkv, G;
+  int32_t R;       // query rows of an item
+  int32_t rc_max;  // row chunks of a sequence, at most
+  int32_t split;   // items may be cut at tiles (partial outputs in the workspace)
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  float* part_out;  // [2 * kMaxGrid][R][D] normalised partial outputs
+  float* part_lse;  // [2 * kMaxGrid][R], log2
+  int2* cuts;       // [batch * Hkv * rc_max]: first CTA and its slot << 16 | CTAs (0: whole)
+  uint32_t* err;
+};
+
+// Launches the kernel for few rows per item (fp4idx_attn_rows.cu).
+fp4idx_status launch_rows(const AttnArgs& a, int head_dim, bool sparse, int grid,
+                          cudaStream_t stream);
+
+}  // namespace fp4idx_impl

@@ -5,8 +5,8 @@ missing: there is no CPU path.  Build it with
 ``python -m fp4_sparse_attention_fp4idx_gb300.build``.
 
 Two layers:
-  * ``lib()`` -- the raw C ABI (names and argument order of include/fp4idx.h,
-    plain integers for pointers).
+  * ``lib()`` -- the raw C ABI (names and argument order of include/fp4idx.h
+    and include/fp4idx_attention.h, plain integers for pointers).
   * torch wrappers with the same names (minus the ``fp4idx_`` prefix) that
     check dtypes/devices, allocate outputs with torch, pass ``data_ptr()``s
     and the current CUDA stream, and raise ``Fp4idxError`` on a non-OK
@@ -22,6 +22,7 @@ import threading
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfp4idx.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp4idx.h")
+ATTENTION_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp4idx_attention.h")
 
 ROPE_NEOX = 0
 ROPE_INTERLEAVED = 1
@@ -78,6 +79,17 @@ _SIGS = {
     "fp4idx_indexer_prepass_host_static": (
         _INT, [_P, _P, _P, _F, _P, _I64, _P, _P, _I64, _F, _P, _P, _P, _P, _P, _P, _I64,
                _INT, _I64, _I64, _P, _P]),
+    "fp4idx_kv_store_fp8": (
+        _INT, [_P, _P, _I64, _I64, _I64, _I64, _INT, _P, _P, _I64, _P, _P]),
+    "fp4idx_kv_load_fp8": (_INT, [_P, _P, _P, _P, _INT, _I64, _P, _P]),
+    "fp4idx_attention_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64]),
+    "fp4idx_paged_attention_fp8": (
+        _INT, [_P, _I64, _I64, _INT, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _F, _P, _P,
+               _I64, _I64, _I64, _P, ctypes.c_size_t, _P, _P]),
+    "fp4idx_sparse_attention_fp8": (
+        _INT, [_P, _I64, _I64, _INT, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _F, _P, _P, _I64,
+               _I64, _I64, _P, ctypes.c_size_t, _P, _P]),
+    "fp4idx_topk_tokens": (_INT, [_P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P]),
     "fp4idx_default_weight_scale": (_F, [_I64]),
     "fp4idx_test_withhold_next": (_INT, [_INT, _I64]),
     "fp4idx_status_string": (ctypes.c_char_p, [_INT]),
@@ -684,3 +696,303 @@ def rope_fake_quant(x, positions, cos_cache, sin_cache, *, rope_style="neox",
         _ptr(err_flags), _stream_ptr(stream))
     _check(st, "fp4idx_rope_fake_quant")
     return out
+
+
+# ------------------------------------- 8-bit key/value cache and its attention
+DTYPE_BF16 = 0
+DTYPE_FP16 = 1
+KV_BLOCK = 64
+
+
+class KvCache(ctypes.Structure):
+    """fp4idx_kv_cache of include/fp4idx_attention.h."""
+    _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_scale", _P), ("v_scale", _P),
+                ("num_blocks", _I64), ("code_block_stride", _I64), ("scale_block_stride", _I64),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+def _stride(t, i, dense):
+    """t.stride(i), or the dense value where a size of 1 leaves it open."""
+    return t.stride(i) if t.shape[i] > 1 else dense
+
+
+def _need16(t, name, ndim):
+    """A CUDA tensor of bf16 or fp16; its fp4idx_dtype code."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    _need(t, t.dtype, name, ndim)
+    return DTYPE_FP16 if t.dtype == torch.float16 else DTYPE_BF16
+
+
+def _one_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale):
+    """The KvCache block of the four tensors."""
+    torch = _torch()
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
+            _need(t, torch.float8_e4m3fn, name, 4)
+        else:
+            _need(t, torch.uint8, name, 4)
+        H, n, D = t.shape[1:]
+        if n != KV_BLOCK or D not in (64, 128):
+            raise ValueError(f"{name} must be [num_blocks, kv_heads, 64, 64 or 128]")
+        if t.stride(3) != 1 or t.stride(2) != D or _stride(t, 1, n * D) != n * D:
+            raise ValueError(f"{name}'s blocks must be dense")
+    _need(k_scale, torch.float32, "k_scale", 2)
+    _need(v_scale, torch.float32, "v_scale", 2)
+    B, H, _, D = k_cache.shape
+    if tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("k_cache and v_cache must have the same shape")
+    if tuple(k_scale.shape) != (B, H) or tuple(v_scale.shape) != (B, H):
+        raise ValueError("k_scale and v_scale must be [num_blocks, kv_heads]")
+    if _stride(k_scale, 1, 1) != 1 or _stride(v_scale, 1, 1) != 1:
+        raise ValueError("k_scale and v_scale must have unit head stride")
+    dense = H * KV_BLOCK * D
+    if _stride(k_cache, 0, dense) != _stride(v_cache, 0, dense) or \
+            _stride(k_scale, 0, H) != _stride(v_scale, 0, H):
+        raise ValueError("keys and values must have the same block strides")
+    _one_device(k_cache.device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                   B, _stride(k_cache, 0, dense), _stride(k_scale, 0, H), H, D)
+
+
+def _need_slots(slot_mapping, T):
+    torch = _torch()
+    _need(slot_mapping, torch.int64, "slot_mapping", 1)
+    if slot_mapping.shape[0] != T or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be contiguous [T]")
+
+
+def _run_on(dev, stream, err_flags):
+    """(device guard, stream pointer) of a call on `dev`."""
+    torch = _torch()
+    if err_flags is not None:
+        _need(err_flags, torch.int32, "err_flags")
+        _one_device(dev, err_flags=err_flags)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    return torch.cuda.device(dev), ctypes.c_void_p(int(s.cuda_stream))
+
+
+def kv_store_fp8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, *, err_flags=None,
+                 stream=None) -> None:
+    """Quantises keys and values into the paged 8-bit cache, in place.  k, v
+    bf16 or fp16 [T, kv_heads, D] (strides multiples of 8), slot_mapping int64
+    [T] (block*64 + offset; negative: skip), k_cache/v_cache uint8 or
+    float8_e4m3fn [num_blocks, kv_heads, 64, D], k_scale/v_scale fp32
+    [num_blocks, kv_heads].  A block's scale covers its 64 tokens; storing
+    behind kept rows grows it where needed and requantises them."""
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    dt = _need16(k, "k", 3)
+    if _need16(v, "v", 3) != dt:
+        raise TypeError("k and v must have the same dtype")
+    T = k.shape[0]
+    if tuple(k.shape[1:]) != (c.kv_heads, c.head_dim) or tuple(v.shape) != tuple(k.shape):
+        raise ValueError("k and v must be [T, kv_heads, D] of the cache's heads and D")
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("k and v must have unit element stride")
+    _need_slots(slot_mapping, T)
+    _one_device(k_cache.device, k=k, v=v, slot_mapping=slot_mapping)
+    guard, s = _run_on(k_cache.device, stream, err_flags)
+    H, D = c.kv_heads, c.head_dim
+    with guard:
+        st = _lib.fp4idx_kv_store_fp8(
+            _ptr(k), _ptr(v), _stride(k, 0, H * D), _stride(k, 1, D), _stride(v, 0, H * D),
+            _stride(v, 1, D), dt, _ptr(slot_mapping), ctypes.byref(c), T, _ptr(err_flags), s)
+    _check(st, "fp4idx_kv_store_fp8")
+
+
+def kv_load_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, *, dtype=None, k_out=None,
+                v_out=None, err_flags=None, stream=None):
+    """Reads cached tokens back -> (k, v) of `dtype` (bf16 by default, or
+    fp16), [T, kv_heads, D].  A negative slot leaves its output row as it was
+    (zeros where the outputs are allocated here)."""
+    torch = _torch()
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    _need(slot_mapping, torch.int64, "slot_mapping", 1)
+    T = slot_mapping.shape[0]
+    _need_slots(slot_mapping, T)
+    outs = []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.zeros((T, c.kv_heads, c.head_dim), device=k_cache.device,
+                            dtype=torch.bfloat16 if dtype is None else dtype)
+        dt = _need16(t, name, 3)
+        if tuple(t.shape) != (T, c.kv_heads, c.head_dim) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous [T, kv_heads, D]")
+        outs.append(t)
+    if outs[0].dtype != outs[1].dtype or (dtype is not None and outs[0].dtype != dtype):
+        raise TypeError("k_out and v_out must have the dtype asked for")
+    _one_device(k_cache.device, k_out=outs[0], v_out=outs[1], slot_mapping=slot_mapping)
+    guard, s = _run_on(k_cache.device, stream, err_flags)
+    with guard:
+        st = _lib.fp4idx_kv_load_fp8(ctypes.byref(c), _ptr(slot_mapping), _ptr(outs[0]),
+                                     _ptr(outs[1]), dt, T, _ptr(err_flags), s)
+    _check(st, "fp4idx_kv_load_fp8")
+    return outs[0], outs[1]
+
+
+def attention_workspace_bytes(batch: int, max_q: int, num_heads: int, kv_heads: int,
+                              head_dim: int) -> int:
+    """Workspace of paged_attention_fp8 (for sparse_attention_fp8: batch = T,
+    max_q = 1); 0 for arguments out of range."""
+    return int(_lib.fp4idx_attention_workspace_bytes(int(batch), int(max_q), int(num_heads),
+                                                     int(kv_heads), int(head_dim)))
+
+
+def _attention_buffers(q, c, block_table, softmax_scale, out, lse, workspace, batch, max_q):
+    torch = _torch()
+    dt = _need16(q, "q", 3)
+    T, H, D = q.shape
+    if D != c.head_dim or q.stride(2) != 1:
+        raise ValueError("q must be [T, H, D] of the cache's D with unit element stride")
+    if H % c.kv_heads:
+        raise ValueError("the query heads must be a multiple of the cache's heads")
+    _need(block_table, torch.int32, "block_table", 2)
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table must have unit column stride")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    _need(out, q.dtype, "out", 3)
+    _need(lse, torch.float32, "lse", 2)
+    if tuple(out.shape) != (T, H, D) or not out.is_contiguous():
+        raise ValueError("out must be contiguous [T, H, D]")
+    if tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous [T, H]")
+    need = attention_workspace_bytes(batch, max_q, H, c.kv_heads, D)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _need(workspace, torch.uint8, "workspace", 1)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _one_device(q.device, block_table=block_table, out=out, lse=lse, workspace=workspace)
+    scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
+    return dt, out, lse, workspace, scale
+
+
+def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
+                        max_context: int, *, q_starts=None, max_q=None, window: int = 0,
+                        sinks: int = 0, softmax_scale=None, out=None, lse=None, workspace=None,
+                        err_flags=None, stream=None):
+    """Causal attention over the 8-bit cache -> (out [T, H, D] of q's dtype,
+    lse fp32 [T, H]).  q bf16 or fp16 [T, H, D]; block_table int32 [batch,
+    pages], context_lens int32 [batch] counts the query tokens too (their keys
+    and values are in the cache).  The query tokens are T / batch per sequence,
+    or, with q_starts int32 [batch+1] and max_q (the longest), ragged.
+    window > 0: a query sees the last `window` keys and the first `sinks`.
+    softmax_scale defaults to D^-1/2."""
+    torch = _torch()
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    _need16(q, "q", 3)
+    _need(context_lens, torch.int32, "context_lens", 1)
+    T, H = q.shape[:2]
+    batch = context_lens.shape[0]
+    if not context_lens.is_contiguous():
+        raise ValueError("context_lens must be contiguous")
+    if q_starts is not None:
+        _need(q_starts, torch.int32, "q_starts", 1)
+        if q_starts.shape[0] != batch + 1 or not q_starts.is_contiguous():
+            raise ValueError("q_starts must be contiguous [batch+1]")
+        if max_q is None:
+            raise ValueError("q_starts needs max_q, the longest sequence of query tokens")
+    else:
+        if (batch == 0 and T > 0) or (batch > 0 and T % batch):
+            raise ValueError("without q_starts, T must be a multiple of the batch")
+        max_q = T // batch if batch else 0
+    if batch and (block_table.dim() != 2 or block_table.shape[0] != batch):
+        raise ValueError("block_table must be [batch, pages]")
+    dt, out, lse, workspace, scale = _attention_buffers(
+        q, c, block_table, softmax_scale, out, lse, workspace, batch, max_q)
+    _one_device(q.device, k_cache=k_cache, context_lens=context_lens, q_starts=q_starts)
+    guard, s = _run_on(q.device, stream, err_flags)
+    pages = block_table.shape[1]
+    with guard:
+        st = _lib.fp4idx_paged_attention_fp8(
+            _ptr(q), _stride(q, 0, H * c.head_dim), _stride(q, 1, c.head_dim), dt, ctypes.byref(c),
+            _ptr(block_table), block_table.stride(0) if batch > 1 else pages, _ptr(context_lens),
+            _ptr(q_starts), int(max_q), int(max_context), int(window), int(sinks), scale,
+            _ptr(out), _ptr(lse), batch, T, H, _ptr(workspace), workspace.numel(),
+            _ptr(err_flags), s)
+    _check(st, "fp4idx_paged_attention_fp8")
+    return out, lse
+
+
+def sparse_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, indices, *,
+                         seq_ids=None, softmax_scale=None, out=None, lse=None, workspace=None,
+                         err_flags=None, stream=None):
+    """Attention over selected tokens of the 8-bit cache -> (out [T, H, D],
+    lse fp32 [T, H]).  indices int32 [T, n]: positions in the token's sequence
+    (negative: left out), as topk_tokens returns them; block_table int32
+    [batch, pages]; seq_ids int32 [T] names each token's sequence (by default
+    T / batch consecutive tokens each)."""
+    torch = _torch()
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    _need16(q, "q", 3)
+    _need(indices, torch.int32, "indices", 2)
+    _need(block_table, torch.int32, "block_table", 2)
+    T, H = q.shape[:2]
+    batch, pages = block_table.shape
+    if indices.shape[0] != T or (indices.shape[1] > 1 and indices.stride(1) != 1):
+        raise ValueError("indices must be [T, n] with unit column stride")
+    if seq_ids is not None:
+        _need(seq_ids, torch.int32, "seq_ids", 1)
+        if seq_ids.shape[0] != T or not seq_ids.is_contiguous():
+            raise ValueError("seq_ids must be contiguous [T]")
+    elif (batch == 0 and T > 0) or (batch > 0 and T % batch):
+        raise ValueError("without seq_ids, T must be a multiple of the batch")
+    dt, out, lse, workspace, scale = _attention_buffers(
+        q, c, block_table, softmax_scale, out, lse, workspace, T, 1)
+    _one_device(q.device, k_cache=k_cache, indices=indices, seq_ids=seq_ids)
+    guard, s = _run_on(q.device, stream, err_flags)
+    n = indices.shape[1]
+    with guard:
+        st = _lib.fp4idx_sparse_attention_fp8(
+            _ptr(q), _stride(q, 0, H * c.head_dim), _stride(q, 1, c.head_dim), dt, ctypes.byref(c),
+            _ptr(block_table), block_table.stride(0) if batch > 1 else pages, pages,
+            _ptr(seq_ids), _ptr(indices), _stride(indices, 0, n), n, scale, _ptr(out), _ptr(lse),
+            batch, T, H, _ptr(workspace), workspace.numel(), _ptr(err_flags), s)
+    _check(st, "fp4idx_sparse_attention_fp8")
+    return out, lse
+
+
+def topk_tokens(logits, k: int, *, row_lens=None, indices=None, counts=None, stream=None):
+    """The k largest logits of each row -> (indices int32 [R, k] ascending,
+    padded with -1, counts int32 [R]).  logits fp32 [R, N] (unit column
+    stride), row_lens int32 [R]: entries behind a row's length are not read;
+    -inf and NaN are never selected, equal logits from the lowest index up."""
+    torch = _torch()
+    _need(logits, torch.float32, "logits", 2)
+    R, N = logits.shape
+    if N > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must have unit column stride")
+    if row_lens is not None:
+        _need(row_lens, torch.int32, "row_lens", 1)
+        if row_lens.shape[0] != R or not row_lens.is_contiguous():
+            raise ValueError("row_lens must be contiguous [R]")
+    if indices is None:
+        indices = torch.empty((R, k), dtype=torch.int32, device=logits.device)
+    if counts is None:
+        counts = torch.empty((R,), dtype=torch.int32, device=logits.device)
+    _need(indices, torch.int32, "indices", 2)
+    _need(counts, torch.int32, "counts", 1)
+    if tuple(indices.shape) != (R, k) or (k > 1 and indices.stride(1) != 1):
+        raise ValueError("indices must be [R, k] with unit column stride")
+    if counts.shape[0] != R or not counts.is_contiguous():
+        raise ValueError("counts must be contiguous [R]")
+    _one_device(logits.device, row_lens=row_lens, indices=indices, counts=counts)
+    guard, s = _run_on(logits.device, stream, None)
+    with guard:
+        st = _lib.fp4idx_topk_tokens(_ptr(logits), _stride(logits, 0, N), _ptr(row_lens),
+                                     _ptr(indices), _stride(indices, 0, k), _ptr(counts), R, N,
+                                     int(k), s)
+    _check(st, "fp4idx_topk_tokens")
+    return indices, counts
