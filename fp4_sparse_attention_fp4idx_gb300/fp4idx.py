@@ -178,9 +178,15 @@ def default_weight_scale(num_heads: int) -> float:
 
 
 # ------------------------------------------------------------ torch wrappers
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream_ptr(stream):
@@ -699,6 +705,9 @@ def rope_fake_quant(x, positions, cos_cache, sin_cache, *, rope_style="neox",
 
 
 # ------------------------------------- 8-bit key/value cache and its attention
+# These calls are made once per layer and step, often on a few microseconds of
+# GPU work, so their checks are written to be cheap: one test per tensor, and
+# plain integers for pointers.
 DTYPE_BF16 = 0
 DTYPE_FP16 = 1
 KV_BLOCK = 64
@@ -711,74 +720,102 @@ class KvCache(ctypes.Structure):
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
-def _stride(t, i, dense):
-    """t.stride(i), or the dense value where a size of 1 leaves it open."""
-    return t.stride(i) if t.shape[i] > 1 else dense
-
-
-def _need16(t, name, ndim):
-    """A CUDA tensor of bf16 or fp16; its fp4idx_dtype code."""
+def _fits(t, dtype, ndim, dev, name):
+    """t is a CUDA tensor of that type and rank on device `dev`."""
     torch = _torch()
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda and t.dim() == ndim):
+        _need(t, dtype, name, ndim)  # says what is wrong
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+
+
+def _dense(t, shape, name):
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {tuple(shape)}")
+
+
+def _type16(t, name):
+    """The fp4idx_dtype code of a tensor of bf16 or fp16."""
+    torch = _torch()
+    dt = getattr(t, "dtype", None)
+    if dt == torch.bfloat16:
+        return DTYPE_BF16
+    if dt == torch.float16:
+        return DTYPE_FP16
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
-    _need(t, t.dtype, name, ndim)
-    return DTYPE_FP16 if t.dtype == torch.float16 else DTYPE_BF16
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {dt}")
 
 
-def _one_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _block_strides(t, n, inner, name):
+    """(block stride, ...) of a [num_blocks, kv_heads, ...] tensor whose heads
+    are `inner` elements apart (a size of 1 leaves its stride open)."""
+    st = t.stride()
+    if n > 1 and st[1] != inner:
+        raise ValueError(f"{name}'s heads must be dense")
+    return st[0] if t.shape[0] > 1 else n * inner
 
 
 def _kv_cache(k_cache, v_cache, k_scale, v_scale):
-    """The KvCache block of the four tensors."""
+    """(KvCache block, device index) of the four tensors."""
     torch = _torch()
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    dev = k_cache.get_device() if isinstance(k_cache, torch.Tensor) else -1
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
-            _need(t, torch.float8_e4m3fn, name, 4)
-        else:
-            _need(t, torch.uint8, name, 4)
-        H, n, D = t.shape[1:]
-        if n != KV_BLOCK or D not in (64, 128):
-            raise ValueError(f"{name} must be [num_blocks, kv_heads, 64, 64 or 128]")
-        if t.stride(3) != 1 or t.stride(2) != D or _stride(t, 1, n * D) != n * D:
-            raise ValueError(f"{name}'s blocks must be dense")
-    _need(k_scale, torch.float32, "k_scale", 2)
-    _need(v_scale, torch.float32, "v_scale", 2)
-    B, H, _, D = k_cache.shape
-    if tuple(v_cache.shape) != tuple(k_cache.shape):
+        _fits(t, f8 if getattr(t, "dtype", None) == f8 else torch.uint8, 4, dev, name)
+    _fits(k_scale, f32, 2, dev, "k_scale")
+    _fits(v_scale, f32, 2, dev, "v_scale")
+    shape = k_cache.shape
+    B, H, n, D = shape
+    if n != KV_BLOCK or D not in (64, 128):
+        raise ValueError("k_cache must be [num_blocks, kv_heads, 64, 64 or 128]")
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    if tuple(k_scale.shape) != (B, H) or tuple(v_scale.shape) != (B, H):
+    if k_scale.shape != (B, H) or v_scale.shape != (B, H):
         raise ValueError("k_scale and v_scale must be [num_blocks, kv_heads]")
-    if _stride(k_scale, 1, 1) != 1 or _stride(v_scale, 1, 1) != 1:
-        raise ValueError("k_scale and v_scale must have unit head stride")
-    dense = H * KV_BLOCK * D
-    if _stride(k_cache, 0, dense) != _stride(v_cache, 0, dense) or \
-            _stride(k_scale, 0, H) != _stride(v_scale, 0, H):
+    if k_cache.stride()[2:] != (D, 1) or v_cache.stride()[2:] != (D, 1):
+        raise ValueError("the rows of a block must be dense")
+    cs = _block_strides(k_cache, H, KV_BLOCK * D, "k_cache")
+    ss = _block_strides(k_scale, H, 1, "k_scale")
+    if _block_strides(v_cache, H, KV_BLOCK * D, "v_cache") != cs or \
+            _block_strides(v_scale, H, 1, "v_scale") != ss:
         raise ValueError("keys and values must have the same block strides")
-    _one_device(k_cache.device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
     return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                   B, _stride(k_cache, 0, dense), _stride(k_scale, 0, H), H, D)
+                   B, cs, ss, H, D), dev
 
 
-def _need_slots(slot_mapping, T):
+def _rows16(t, H, D, dev, name):
+    """(token stride, head stride) of a 16-bit [T, H, D] tensor."""
+    _fits(t, t.dtype, 3, dev, name)
+    T, h, d = t.shape
+    st = t.stride()
+    if h != H or d != D or st[2] != 1:
+        raise ValueError(f"{name} must be [T, {H}, {D}] with unit element stride")
+    return (st[0] if T > 1 else H * D), (st[1] if H > 1 else D)
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with `dev` the current device; raises on a status."""
     torch = _torch()
-    _need(slot_mapping, torch.int64, "slot_mapping", 1)
-    if slot_mapping.shape[0] != T or not slot_mapping.is_contiguous():
-        raise ValueError("slot_mapping must be contiguous [T]")
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != OK:
+        raise Fp4idxError(st, fn.__name__)
 
 
-def _run_on(dev, stream, err_flags):
-    """(device guard, stream pointer) of a call on `dev`."""
+def _flags(err_flags, dev):
+    if err_flags is None:
+        return None
     torch = _torch()
-    if err_flags is not None:
-        _need(err_flags, torch.int32, "err_flags")
-        _one_device(dev, err_flags=err_flags)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    return torch.cuda.device(dev), ctypes.c_void_p(int(s.cuda_stream))
+    _fits(err_flags, torch.int32, err_flags.dim() if isinstance(err_flags, torch.Tensor) else 1,
+          dev, "err_flags")
+    if err_flags.numel() < 1:
+        raise ValueError("err_flags must hold an element")
+    return err_flags.data_ptr()
 
 
 def kv_store_fp8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, *, err_flags=None,
@@ -789,24 +826,21 @@ def kv_store_fp8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, *, err_
     float8_e4m3fn [num_blocks, kv_heads, 64, D], k_scale/v_scale fp32
     [num_blocks, kv_heads].  A block's scale covers its 64 tokens; storing
     behind kept rows grows it where needed and requantises them."""
-    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    dt = _need16(k, "k", 3)
-    if _need16(v, "v", 3) != dt:
+    torch = _torch()
+    c, dev = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    dt = _type16(k, "k")
+    if _type16(v, "v") != dt:
         raise TypeError("k and v must have the same dtype")
-    T = k.shape[0]
-    if tuple(k.shape[1:]) != (c.kv_heads, c.head_dim) or tuple(v.shape) != tuple(k.shape):
-        raise ValueError("k and v must be [T, kv_heads, D] of the cache's heads and D")
-    if k.stride(2) != 1 or v.stride(2) != 1:
-        raise ValueError("k and v must have unit element stride")
-    _need_slots(slot_mapping, T)
-    _one_device(k_cache.device, k=k, v=v, slot_mapping=slot_mapping)
-    guard, s = _run_on(k_cache.device, stream, err_flags)
     H, D = c.kv_heads, c.head_dim
-    with guard:
-        st = _lib.fp4idx_kv_store_fp8(
-            _ptr(k), _ptr(v), _stride(k, 0, H * D), _stride(k, 1, D), _stride(v, 0, H * D),
-            _stride(v, 1, D), dt, _ptr(slot_mapping), ctypes.byref(c), T, _ptr(err_flags), s)
-    _check(st, "fp4idx_kv_store_fp8")
+    kt, kh = _rows16(k, H, D, dev, "k")
+    vt, vh = _rows16(v, H, D, dev, "v")
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same tokens")
+    _fits(slot_mapping, torch.int64, 1, dev, "slot_mapping")
+    _dense(slot_mapping, (T,), "slot_mapping")
+    _call(_lib.fp4idx_kv_store_fp8, dev, stream, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, dt,
+          slot_mapping.data_ptr(), ctypes.byref(c), T, _flags(err_flags, dev))
 
 
 def kv_load_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, *, dtype=None, k_out=None,
@@ -815,68 +849,65 @@ def kv_load_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, *, dtype=None,
     fp16), [T, kv_heads, D].  A negative slot leaves its output row as it was
     (zeros where the outputs are allocated here)."""
     torch = _torch()
-    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    _need(slot_mapping, torch.int64, "slot_mapping", 1)
+    c, dev = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    _fits(slot_mapping, torch.int64, 1, dev, "slot_mapping")
     T = slot_mapping.shape[0]
-    _need_slots(slot_mapping, T)
-    outs = []
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = torch.zeros((T, c.kv_heads, c.head_dim), device=k_cache.device,
-                            dtype=torch.bfloat16 if dtype is None else dtype)
-        dt = _need16(t, name, 3)
-        if tuple(t.shape) != (T, c.kv_heads, c.head_dim) or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous [T, kv_heads, D]")
-        outs.append(t)
-    if outs[0].dtype != outs[1].dtype or (dtype is not None and outs[0].dtype != dtype):
-        raise TypeError("k_out and v_out must have the dtype asked for")
-    _one_device(k_cache.device, k_out=outs[0], v_out=outs[1], slot_mapping=slot_mapping)
-    guard, s = _run_on(k_cache.device, stream, err_flags)
-    with guard:
-        st = _lib.fp4idx_kv_load_fp8(ctypes.byref(c), _ptr(slot_mapping), _ptr(outs[0]),
-                                     _ptr(outs[1]), dt, T, _ptr(err_flags), s)
-    _check(st, "fp4idx_kv_load_fp8")
-    return outs[0], outs[1]
+    _dense(slot_mapping, (T,), "slot_mapping")
+    shape = (T, c.kv_heads, c.head_dim)
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else \
+            v_out.dtype if v_out is not None else torch.bfloat16
+    if k_out is None:
+        k_out = torch.zeros(shape, device=k_cache.device, dtype=dtype)
+    if v_out is None:
+        v_out = torch.zeros(shape, device=k_cache.device, dtype=dtype)
+    dt = _type16(k_out, "k_out")
+    _fits(k_out, dtype, 3, dev, "k_out")
+    _fits(v_out, dtype, 3, dev, "v_out")
+    _dense(k_out, shape, "k_out")
+    _dense(v_out, shape, "v_out")
+    _call(_lib.fp4idx_kv_load_fp8, dev, stream, ctypes.byref(c), slot_mapping.data_ptr(),
+          k_out.data_ptr(), v_out.data_ptr(), dt, T, _flags(err_flags, dev))
+    return k_out, v_out
 
 
 def attention_workspace_bytes(batch: int, max_q: int, num_heads: int, kv_heads: int,
                               head_dim: int) -> int:
     """Workspace of paged_attention_fp8 (for sparse_attention_fp8: batch = T,
     max_q = 1); 0 for arguments out of range."""
-    return int(_lib.fp4idx_attention_workspace_bytes(int(batch), int(max_q), int(num_heads),
-                                                     int(kv_heads), int(head_dim)))
+    return _lib.fp4idx_attention_workspace_bytes(batch, max_q, num_heads, kv_heads, head_dim)
 
 
-def _attention_buffers(q, c, block_table, softmax_scale, out, lse, workspace, batch, max_q):
+def _attention_buffers(q, c, dev, block_table, out, lse, workspace, batch, max_q):
+    """Checks of q and block_table; (dtype code, strides of q, out, lse,
+    workspace), allocated where not given."""
     torch = _torch()
-    dt = _need16(q, "q", 3)
-    T, H, D = q.shape
-    if D != c.head_dim or q.stride(2) != 1:
-        raise ValueError("q must be [T, H, D] of the cache's D with unit element stride")
-    if H % c.kv_heads:
-        raise ValueError("the query heads must be a multiple of the cache's heads")
-    _need(block_table, torch.int32, "block_table", 2)
+    dt = _type16(q, "q")
+    D = c.head_dim
+    if q.dim() != 3 or q.shape[1] % c.kv_heads:
+        raise ValueError("q must be [T, H, D], H a multiple of the cache's heads")
+    T, H = q.shape[0], q.shape[1]
+    qt, qh = _rows16(q, H, D, dev, "q")
+    _fits(block_table, torch.int32, 2, dev, "block_table")
     if block_table.shape[1] > 1 and block_table.stride(1) != 1:
         raise ValueError("block_table must have unit column stride")
     if out is None:
         out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    else:
+        _fits(out, q.dtype, 3, dev, "out")
+        _dense(out, (T, H, D), "out")
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    _need(out, q.dtype, "out", 3)
-    _need(lse, torch.float32, "lse", 2)
-    if tuple(out.shape) != (T, H, D) or not out.is_contiguous():
-        raise ValueError("out must be contiguous [T, H, D]")
-    if tuple(lse.shape) != (T, H) or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous [T, H]")
-    need = attention_workspace_bytes(batch, max_q, H, c.kv_heads, D)
+    else:
+        _fits(lse, torch.float32, 2, dev, "lse")
+        _dense(lse, (T, H), "lse")
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    _need(workspace, torch.uint8, "workspace", 1)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _one_device(q.device, block_table=block_table, out=out, lse=lse, workspace=workspace)
-    scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
-    return dt, out, lse, workspace, scale
+        need = _lib.fp4idx_attention_workspace_bytes(batch, max_q, H, c.kv_heads, D)
+        workspace = torch.empty(need or 16, dtype=torch.uint8, device=q.device)
+    else:
+        _fits(workspace, torch.uint8, 1, dev, "workspace")
+        _dense(workspace, workspace.shape, "workspace")
+    return dt, qt, qh, out, lse, workspace
 
 
 def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
@@ -891,38 +922,32 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cont
     window > 0: a query sees the last `window` keys and the first `sinks`.
     softmax_scale defaults to D^-1/2."""
     torch = _torch()
-    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    _need16(q, "q", 3)
-    _need(context_lens, torch.int32, "context_lens", 1)
-    T, H = q.shape[:2]
-    batch = context_lens.shape[0]
-    if not context_lens.is_contiguous():
-        raise ValueError("context_lens must be contiguous")
+    c, dev = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    _type16(q, "q")
+    _fits(context_lens, torch.int32, 1, dev, "context_lens")
+    T, batch = q.shape[0], context_lens.shape[0]
+    _dense(context_lens, (batch,), "context_lens")
+    starts = None
     if q_starts is not None:
-        _need(q_starts, torch.int32, "q_starts", 1)
-        if q_starts.shape[0] != batch + 1 or not q_starts.is_contiguous():
-            raise ValueError("q_starts must be contiguous [batch+1]")
+        _fits(q_starts, torch.int32, 1, dev, "q_starts")
+        _dense(q_starts, (batch + 1,), "q_starts")
         if max_q is None:
             raise ValueError("q_starts needs max_q, the longest sequence of query tokens")
+        starts = q_starts.data_ptr()
     else:
         if (batch == 0 and T > 0) or (batch > 0 and T % batch):
             raise ValueError("without q_starts, T must be a multiple of the batch")
         max_q = T // batch if batch else 0
-    if batch and (block_table.dim() != 2 or block_table.shape[0] != batch):
+    dt, qt, qh, out, lse, workspace = _attention_buffers(q, c, dev, block_table, out, lse,
+                                                         workspace, batch, max_q)
+    if block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, pages]")
-    dt, out, lse, workspace, scale = _attention_buffers(
-        q, c, block_table, softmax_scale, out, lse, workspace, batch, max_q)
-    _one_device(q.device, k_cache=k_cache, context_lens=context_lens, q_starts=q_starts)
-    guard, s = _run_on(q.device, stream, err_flags)
-    pages = block_table.shape[1]
-    with guard:
-        st = _lib.fp4idx_paged_attention_fp8(
-            _ptr(q), _stride(q, 0, H * c.head_dim), _stride(q, 1, c.head_dim), dt, ctypes.byref(c),
-            _ptr(block_table), block_table.stride(0) if batch > 1 else pages, _ptr(context_lens),
-            _ptr(q_starts), int(max_q), int(max_context), int(window), int(sinks), scale,
-            _ptr(out), _ptr(lse), batch, T, H, _ptr(workspace), workspace.numel(),
-            _ptr(err_flags), s)
-    _check(st, "fp4idx_paged_attention_fp8")
+    _call(_lib.fp4idx_paged_attention_fp8, dev, stream, q.data_ptr(), qt, qh, dt, ctypes.byref(c),
+          block_table.data_ptr(), block_table.stride(0) if batch > 1 else block_table.shape[1],
+          context_lens.data_ptr(), starts, max_q, max_context, window, sinks,
+          c.head_dim ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(),
+          lse.data_ptr(), batch, T, q.shape[1], workspace.data_ptr(), workspace.numel(),
+          _flags(err_flags, dev))
     return out, lse
 
 
@@ -935,32 +960,29 @@ def sparse_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, ind
     [batch, pages]; seq_ids int32 [T] names each token's sequence (by default
     T / batch consecutive tokens each)."""
     torch = _torch()
-    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    _need16(q, "q", 3)
-    _need(indices, torch.int32, "indices", 2)
-    _need(block_table, torch.int32, "block_table", 2)
-    T, H = q.shape[:2]
-    batch, pages = block_table.shape
-    if indices.shape[0] != T or (indices.shape[1] > 1 and indices.stride(1) != 1):
+    c, dev = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    _type16(q, "q")
+    T = q.shape[0]
+    _fits(indices, torch.int32, 2, dev, "indices")
+    n = indices.shape[1]
+    if indices.shape[0] != T or (n > 1 and indices.stride(1) != 1):
         raise ValueError("indices must be [T, n] with unit column stride")
+    dt, qt, qh, out, lse, workspace = _attention_buffers(q, c, dev, block_table, out, lse,
+                                                         workspace, T, 1)
+    batch, pages = block_table.shape
+    seqs = None
     if seq_ids is not None:
-        _need(seq_ids, torch.int32, "seq_ids", 1)
-        if seq_ids.shape[0] != T or not seq_ids.is_contiguous():
-            raise ValueError("seq_ids must be contiguous [T]")
+        _fits(seq_ids, torch.int32, 1, dev, "seq_ids")
+        _dense(seq_ids, (T,), "seq_ids")
+        seqs = seq_ids.data_ptr()
     elif (batch == 0 and T > 0) or (batch > 0 and T % batch):
         raise ValueError("without seq_ids, T must be a multiple of the batch")
-    dt, out, lse, workspace, scale = _attention_buffers(
-        q, c, block_table, softmax_scale, out, lse, workspace, T, 1)
-    _one_device(q.device, k_cache=k_cache, indices=indices, seq_ids=seq_ids)
-    guard, s = _run_on(q.device, stream, err_flags)
-    n = indices.shape[1]
-    with guard:
-        st = _lib.fp4idx_sparse_attention_fp8(
-            _ptr(q), _stride(q, 0, H * c.head_dim), _stride(q, 1, c.head_dim), dt, ctypes.byref(c),
-            _ptr(block_table), block_table.stride(0) if batch > 1 else pages, pages,
-            _ptr(seq_ids), _ptr(indices), _stride(indices, 0, n), n, scale, _ptr(out), _ptr(lse),
-            batch, T, H, _ptr(workspace), workspace.numel(), _ptr(err_flags), s)
-    _check(st, "fp4idx_sparse_attention_fp8")
+    _call(_lib.fp4idx_sparse_attention_fp8, dev, stream, q.data_ptr(), qt, qh, dt, ctypes.byref(c),
+          block_table.data_ptr(), block_table.stride(0) if batch > 1 else pages, pages, seqs,
+          indices.data_ptr(), indices.stride(0) if T > 1 else n, n,
+          c.head_dim ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(),
+          lse.data_ptr(), batch, T, q.shape[1], workspace.data_ptr(), workspace.numel(),
+          _flags(err_flags, dev))
     return out, lse
 
 
@@ -970,29 +992,28 @@ def topk_tokens(logits, k: int, *, row_lens=None, indices=None, counts=None, str
     stride), row_lens int32 [R]: entries behind a row's length are not read;
     -inf and NaN are never selected, equal logits from the lowest index up."""
     torch = _torch()
-    _need(logits, torch.float32, "logits", 2)
+    dev = logits.get_device() if isinstance(logits, torch.Tensor) else -1
+    _fits(logits, torch.float32, 2, dev, "logits")
     R, N = logits.shape
     if N > 1 and logits.stride(1) != 1:
         raise ValueError("logits must have unit column stride")
+    lens = None
     if row_lens is not None:
-        _need(row_lens, torch.int32, "row_lens", 1)
-        if row_lens.shape[0] != R or not row_lens.is_contiguous():
-            raise ValueError("row_lens must be contiguous [R]")
+        _fits(row_lens, torch.int32, 1, dev, "row_lens")
+        _dense(row_lens, (R,), "row_lens")
+        lens = row_lens.data_ptr()
     if indices is None:
         indices = torch.empty((R, k), dtype=torch.int32, device=logits.device)
+    else:
+        _fits(indices, torch.int32, 2, dev, "indices")
+        if indices.shape != (R, k) or (k > 1 and indices.stride(1) != 1):
+            raise ValueError("indices must be [R, k] with unit column stride")
     if counts is None:
         counts = torch.empty((R,), dtype=torch.int32, device=logits.device)
-    _need(indices, torch.int32, "indices", 2)
-    _need(counts, torch.int32, "counts", 1)
-    if tuple(indices.shape) != (R, k) or (k > 1 and indices.stride(1) != 1):
-        raise ValueError("indices must be [R, k] with unit column stride")
-    if counts.shape[0] != R or not counts.is_contiguous():
-        raise ValueError("counts must be contiguous [R]")
-    _one_device(logits.device, row_lens=row_lens, indices=indices, counts=counts)
-    guard, s = _run_on(logits.device, stream, None)
-    with guard:
-        st = _lib.fp4idx_topk_tokens(_ptr(logits), _stride(logits, 0, N), _ptr(row_lens),
-                                     _ptr(indices), _stride(indices, 0, k), _ptr(counts), R, N,
-                                     int(k), s)
-    _check(st, "fp4idx_topk_tokens")
+    else:
+        _fits(counts, torch.int32, 1, dev, "counts")
+        _dense(counts, (R,), "counts")
+    _call(_lib.fp4idx_topk_tokens, dev, stream, logits.data_ptr(),
+          logits.stride(0) if R > 1 else N, lens, indices.data_ptr(),
+          indices.stride(0) if R > 1 else k, counts.data_ptr(), R, N, k)
     return indices, counts
