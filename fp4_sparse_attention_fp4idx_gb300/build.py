@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", name)
         for name in ("fp4idx.cu", "fp4idx_stream.cu", "fp4idx_scorer.cu", "fp4idx_host.cu",
                      "fp4idx_kvcache.cu", "fp4idx_topk.cu", "fp4idx_attn.cu",
-                     "fp4idx_attn_rows.cu")]
+                     "fp4idx_attn_rows.cu", "fp4idx_attn_tiles.cu")]
 HDRS = [*(os.path.join(ROOT, "include", name) for name in ("fp4idx.h", "fp4idx_attention.h")),
         *(os.path.join(PKG, "csrc", name) for name in ("fp4idx_common.cuh",
                                                        "fp4idx_attention_common.cuh",

@@ -9,21 +9,39 @@ namespace {
 
 constexpr int kPage = FP4IDX_KV_BLOCK;
 
-// Query rows of an item: the least of 8, 16 and 32 that holds `rows`.
-int item_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// From this many query rows per sequence and key head on, the tensor-core
+// kernel of 256-row items (fp4idx_attn_tiles.cu) takes the call.
+constexpr int64_t kTileFrom = 128;
+constexpr int64_t kTileRows = 256;
+
+// Query rows of an item; selected tokens never take the tensor-core kernel.
+int64_t item_rows(int64_t rows, bool sparse) {
+  return !sparse && rows >= kTileFrom ? kTileRows : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+
+// Key ranges of an item of the tensor-core kernel, at most: as many as fill
+// the GPU once.
+int64_t tile_splits(int64_t items) { return items < kMaxGrid ? kMaxGrid / items : 1; }
 
 struct Workspace {
   int64_t part_lse, cuts, total;  // offsets in bytes; partial outputs at 0
 };
 
 Workspace workspace_of(int64_t batch, int64_t max_q, int64_t num_heads, int64_t kv_heads,
-                       int64_t head_dim) {
+                       int64_t head_dim, bool sparse) {
   const int64_t rows = max_q * (num_heads / kv_heads);
-  const int64_t R = item_rows(rows);
+  const int64_t R = item_rows(rows, sparse);
+  const int64_t items = batch * kv_heads * ((rows + R - 1) / R);
+  int64_t slots = 2 * kMaxGrid, cuts = items * 8;
+  if (R == kTileRows) {
+    const int64_t splits = items > 0 ? tile_splits(items) : 1;
+    slots = splits > 1 ? items * splits : 0;
+    cuts = 0;
+  }
   Workspace w;
-  w.part_lse = 2 * kMaxGrid * R * head_dim * 4;
-  w.cuts = w.part_lse + 2 * kMaxGrid * R * 4;
-  w.total = (w.cuts + batch * kv_heads * ((rows + R - 1) / R) * 8 + 255) / 256 * 256;
+  w.part_lse = slots * R * head_dim * 4;
+  w.cuts = w.part_lse + slots * R * 4;
+  w.total = (w.cuts + cuts + 256) / 256 * 256;
   return w;
 }
 
@@ -42,14 +60,15 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
                           const int32_t* block_table, int64_t block_table_stride,
                           float softmax_scale, void* out, float* lse, int64_t items,
                           int64_t max_q, int64_t num_tokens, int64_t num_heads, void* workspace,
-                          size_t workspace_bytes, uint32_t* err_flags) {
+                          size_t workspace_bytes, uint32_t* err_flags, bool sparse) {
   const fp4idx_status cs = check_cache(cache);
   if (cs == FP4IDX_ERR_NULL || !q || !block_table || !out || !workspace) return FP4IDX_ERR_NULL;
   if (cs == FP4IDX_ERR_SHAPE || num_heads < 1 || num_heads % cache->kv_heads ||
       num_tokens >= (1ll << 31) ||
       !workspace_args_ok(items, max_q, num_heads, cache->kv_heads, cache->head_dim))
     return FP4IDX_ERR_SHAPE;
-  const Workspace w = workspace_of(items, max_q, num_heads, cache->kv_heads, cache->head_dim);
+  const Workspace w = workspace_of(items, max_q, num_heads, cache->kv_heads, cache->head_dim,
+                                   sparse);
   if (workspace_bytes < (size_t)w.total) return FP4IDX_ERR_SCRATCH;
   if (!dtype_ok(dtype) || !isfinite(softmax_scale)) return FP4IDX_ERR_ARG;
   if (cs != FP4IDX_OK || !aligned(q, 16) || q_token_stride % 8 || q_head_stride % 8 ||
@@ -75,7 +94,7 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
   a.Hq = (int32_t)num_heads;
   a.Hkv = cache->kv_heads;
   a.G = (int32_t)(num_heads / cache->kv_heads);
-  a.R = item_rows(max_q * a.G);
+  a.R = (int32_t)item_rows(max_q * a.G, sparse);
   a.rc_max = (int32_t)((max_q * a.G + a.R - 1) / a.R);
   a.scale_log2 = softmax_scale * kLog2e;
   a.out = static_cast<uint16_t*>(out);
@@ -88,10 +107,17 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
   return FP4IDX_OK;
 }
 
-// Items of few tiles are not worth cutting: the join costs more than it saves.
+// `max_tiles`: 64-key tiles of an item, at most.
 fp4idx_status launch(AttnArgs& a, int head_dim, bool sparse, int64_t max_tiles, void* stream) {
-  a.split = max_tiles > 8;
   const int64_t items = (int64_t)a.batch * a.Hkv * a.rc_max;
+  if (a.R == kTileRows) {
+    const int64_t most = (max_tiles + 7) / 8, splits = tile_splits(items);
+    a.splits = (int32_t)(splits < most ? splits : most);
+    if (items * a.splits >= (1ll << 31)) return FP4IDX_ERR_SHAPE;
+    return launch_tiles(a, head_dim, static_cast<cudaStream_t>(stream));
+  }
+  // items of few tiles are not worth cutting: the join costs more than it saves
+  a.split = max_tiles > 8;
   const int64_t units = a.split ? items * max_tiles : items;
   const int grid = units < kMaxGrid ? (int)units : kMaxGrid;
   return launch_rows(a, head_dim, sparse, grid, static_cast<cudaStream_t>(stream));
@@ -106,7 +132,10 @@ extern "C" size_t fp4idx_attention_workspace_bytes(int64_t batch, int64_t max_q,
                                                    int64_t num_heads, int64_t kv_heads,
                                                    int64_t head_dim) {
   if (!workspace_args_ok(batch, max_q, num_heads, kv_heads, head_dim)) return 0;
-  return (size_t)workspace_of(batch, max_q, num_heads, kv_heads, head_dim).total;
+  // the larger of the two forms' needs
+  const int64_t dense = workspace_of(batch, max_q, num_heads, kv_heads, head_dim, false).total;
+  const int64_t sparse = workspace_of(batch, max_q, num_heads, kv_heads, head_dim, true).total;
+  return (size_t)(dense > sparse ? dense : sparse);
 }
 
 extern "C" fp4idx_status fp4idx_paged_attention_fp8(
@@ -132,7 +161,7 @@ extern "C" fp4idx_status fp4idx_paged_attention_fp8(
   const fp4idx_status st =
       common_args(a, q, q_token_stride, q_head_stride, dtype, cache, block_table,
                   block_table_stride, softmax_scale, out, lse, batch, max_q, num_tokens, num_heads,
-                  workspace, workspace_bytes, err_flags);
+                  workspace, workspace_bytes, err_flags, false);
   if (st != FP4IDX_OK) return st;
   if (!aligned(context_lens, 4) || !aligned(q_starts, 4)) return FP4IDX_ERR_ALIGN;
   a.ctx = context_lens;
@@ -168,7 +197,7 @@ extern "C" fp4idx_status fp4idx_sparse_attention_fp8(
   const fp4idx_status st = common_args(a, q, q_token_stride, q_head_stride, dtype, cache,
                                        block_table, block_table_stride, softmax_scale, out, lse,
                                        num_tokens, 1, num_tokens, num_heads, workspace,
-                                       workspace_bytes, err_flags);
+                                       workspace_bytes, err_flags, true);
   if (st != FP4IDX_OK) return st;
   if (!aligned(seq_ids, 4) || !aligned(indices, 4)) return FP4IDX_ERR_ALIGN;
   a.seq_ids = seq_ids;

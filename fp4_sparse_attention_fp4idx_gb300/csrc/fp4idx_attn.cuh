@@ -2,6 +2,8 @@
 // (fp4idx_attn.cu) and their kernels share.
 #pragma once
 
+#include <atomic>
+
 #include "fp4idx_attention_common.cuh"
 
 namespace fp4idx_impl {
@@ -32,12 +34,13 @@ struct AttnArgs {
   int32_t batch, T, Hq, Hkv, G;
   int32_t R;       // query rows of an item
   int32_t rc_max;  // row chunks of a sequence, at most
+  int32_t splits;  // key ranges of an item (fp4idx_attn_tiles.cu)
   int32_t split;   // items may be cut at tiles (partial outputs in the workspace)
   float scale_log2;
   uint16_t* out;
   float* lse;
-  float* part_out;  // [2 * kMaxGrid][R][D] normalised partial outputs
-  float* part_lse;  // [2 * kMaxGrid][R], log2
+  float* part_out;  // [slot][R][D] normalised partial outputs
+  float* part_lse;  // [slot][R], log2
   int2* cuts;       // [batch * Hkv * rc_max]: first CTA and its slot << 16 | CTAs (0: whole)
   uint32_t* err;
 };
@@ -45,5 +48,44 @@ struct AttnArgs {
 // Launches the kernel for few rows per item (fp4idx_attn_rows.cu).
 fp4idx_status launch_rows(const AttnArgs& a, int head_dim, bool sparse, int grid,
                           cudaStream_t stream);
+
+// Launches the kernel for many rows per item (fp4idx_attn_tiles.cu).
+fp4idx_status launch_tiles(const AttnArgs& a, int head_dim, cudaStream_t stream);
+
+// Raises a kernel's dynamic shared-memory limit, once per device.
+class SmemOnce {
+ public:
+  template <typename Kernel>
+  bool set(Kernel* kern, int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (done_.load(std::memory_order_acquire) >> dev & 1u) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+      return false;
+    done_.fetch_or(1ull << dev, std::memory_order_release);
+    return true;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
+
+// Launches kern behind the stream's last kernel, allowed to start early: it
+// waits for that kernel's results itself (griddepcontrol.wait).
+template <typename Args>
+inline cudaError_t launch_after(void (*kern)(Args), unsigned grid, unsigned block,
+                                cudaStream_t stream, const Args& a) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
 
 }  // namespace fp4idx_impl

@@ -831,23 +831,15 @@ fp4idx_status launch_one(const AttnArgs& a, int grid, cudaStream_t stream) {
   auto* kern = rows_kernel<D, NT, kSparse>;
   constexpr int bytes = smem_bytes(D, NT);
   static_assert(bytes + 2048 <= 227 * 1024, "the rings fit the shared memory");
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-      cudaSuccess)
-    return FP4IDX_ERR_CUDA;
+  static SmemOnce once;
+  if (!once.set(kern, bytes)) return FP4IDX_ERR_CUDA;
   if (launch_kernel(kern, (unsigned)grid, kThreads, bytes, stream, a) != cudaSuccess)
     return FP4IDX_ERR_CUDA;
   if (!a.split) return FP4IDX_OK;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.batch * a.Hkv * a.rc_max));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, kSparse>, a) == cudaSuccess ? FP4IDX_OK
-                                                                             : FP4IDX_ERR_CUDA;
+  return launch_after(join_kernel<D, kSparse>, (unsigned)((int64_t)a.batch * a.Hkv * a.rc_max),
+                      128, stream, a) == cudaSuccess
+             ? FP4IDX_OK
+             : FP4IDX_ERR_CUDA;
 }
 
 template <int D, bool kSparse>

@@ -84,14 +84,16 @@ def check(out, lse, ref, n):
 
     A score is a sum of <= 128 exact products in fp32 (each partial sum within
     2^-24 of sum|q k|, at most 2^-17 in all, doubled for the tensor core's
-    truncating alignment), a probability is rounded to fp16 (2^-11 of itself,
-    or 2^-39 of the largest contribution, taken here as max sum p|v| over d),
+    truncating alignment), a probability is rounded to fp16 (2^-11 of itself;
+    or half the least subnormal, 2^-25, of a scale where the row's largest
+    contribution is at least 2^10, times a code of at most 448: taken here as
+    2^-34 * 448 of max sum p|v| over d),
     ex2.approx and the fp32 sums add less than 2^-19, and the output is rounded
     once to its type."""
     o, e, pv, top = ref
     u = torch.finfo(out.dtype).eps / 2
     d_score = 2.0 ** -16 * top + 2.0 ** -19
-    tiny = 2.0 ** -38 * n * 448 * pv.amax(-1, keepdim=True) + torch.finfo(out.dtype).tiny * u
+    tiny = 2.0 ** -34 * 448 * n * pv.amax(-1, keepdim=True) + torch.finfo(out.dtype).tiny * u
     tol = u * o.abs() + (1 + u) * (pv * (2.0 ** -11 + 2 * d_score[:, None]) + tiny)
     err = (out.double() - o).abs()
     bad = ~(err <= tol)

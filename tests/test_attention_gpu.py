@@ -78,6 +78,78 @@ def test_ragged_prefill(window, sinks, Hq, Hkv, D, dtype):
     run_dense(ctx, qs, Hq, Hkv, D, dtype, window, sinks, seed=window + Hq)
 
 
+@pytest.mark.parametrize("ctx,qs", [([128], [128]), ([129], [129]), ([1], [1]), ([300], [40]),
+                                    ([1000, 77], [64, 77]), ([513, 0, 640], [513, 0, 5]),
+                                    ([2000], [33])])
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,window,sinks", [
+    (8, 2, 128, BF, 0, 0), (3, 1, 64, HF, 0, 0), (5, 1, 128, HF, 130, 0), (8, 1, 64, BF, 50, 200),
+    (130, 1, 128, BF, 0, 0), (260, 2, 64, BF, 300, 4), (1, 1, 128, BF, 1, 1)])
+def test_prompts(ctx, qs, Hq, Hkv, D, dtype, window, sinks):
+    """Chunks and whole prompts, up to 1,200 rows a key head: the tensor-core
+    kernel's row halves, tile borders, masks and key ranges."""
+    run_dense(ctx, qs, Hq, Hkv, D, dtype, window, sinks, seed=Hq + window + sum(ctx))
+
+
+def test_prompt_longer_than_the_context_it_is_given():
+    """A context shorter than the chunk leaves the first rows without a key."""
+    run_dense([100, 40, 0], [160, 160, 160], 4, 1, 128, BF, ragged=False, seed=2)
+
+
+def test_tokens_behind_max_q_are_left_unwritten():
+    ctx, D = [400], 64
+    q, cache, table, starts = setup(ctx, [200], 4, 2, D, BF, 31)
+    for max_q in (7, 100):
+        out = torch.full((200, 4, D), 3.0, dtype=BF, device="cuda")
+        lse = torch.full((200, 4), 3.0, device="cuda")
+        F().paged_attention_fp8(q, *cache, table, i32(ctx), 400, q_starts=i32(starts), max_q=max_q,
+                                out=out, lse=lse)
+        ref = R.dense(q, cache, table, ctx, starts, 0, 0, D ** -0.5)
+        ref = tuple(x.view(200, 4, -1)[:max_q].reshape(-1, *x.shape[1:]) for x in ref)
+        R.check(out[:max_q].reshape(-1, D), lse[:max_q].reshape(-1), ref, 401)
+        assert bool((out[max_q:] == 3.0).all()) and bool((lse[max_q:] == 3.0).all())
+
+
+@pytest.mark.parametrize("bad", [-1, 2 ** 31 - 1])
+def test_bad_pages_in_a_prompt(bad):
+    ctx, D, n = [500], 128, 50
+    q, cache, table, starts = setup(ctx, [n], 8, 2, D, BF, 32)
+    t = table.clone()
+    t[0, 3] = bad
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = F().paged_attention_fp8(q, *cache, t, i32(ctx), 500, err_flags=err)
+    assert int(err.item()) == ERR_PAGE
+    idx = torch.full((n, 500), -1, dtype=torch.int32)
+    for i in range(n):
+        keep = [s for s in range(500 - n + i + 1) if s // 64 != 3]
+        idx[i, :len(keep)] = torch.tensor(keep, dtype=torch.int32)
+    ref = R.sparse(q, cache, table, idx.cuda(), [0] * n, D ** -0.5)
+    R.check(out.view(-1, D), lse.view(-1), ref, 501)
+
+
+@pytest.mark.parametrize("mag,scale", [(30.0, None), (1e-3, -0.5), (1.0, 0.0)])
+def test_prompt_magnitudes_and_scales(mag, scale):
+    ctx, D = [333, 260], 128
+    q, cache, table, starts = setup(ctx, [64, 64], 8, 2, D, BF, 5)
+    q = (q.float() * mag).to(BF)
+    out, lse = F().paged_attention_fp8(q, *cache, table, i32(ctx), 333, softmax_scale=scale)
+    ref = R.dense(q, cache, table, ctx, starts, 0, 0, D ** -0.5 if scale is None else scale)
+    R.check(out.view(-1, D), lse.view(-1), ref, 334)
+
+
+def test_prompt_deterministic_and_captured():
+    ctx, D = [3000], 128
+    q, cache, table, starts = setup(ctx, [100], 8, 2, D, BF, 41)
+    first = F().paged_attention_fp8(q, *cache, table, i32(ctx), 3000)
+    graph = torch.cuda.CUDAGraph()
+    lens = i32(ctx)
+    with torch.cuda.graph(graph):
+        got = F().paged_attention_fp8(q, *cache, table, lens, 3000)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,dtype,n", [(8, 1, 128, BF, 1), (16, 2, 64, HF, 1),
                                               (4, 4, 128, BF, 3), (32, 1, 128, BF, 1)])
 def test_long_contexts_are_split_and_joined(Hq, Hkv, D, dtype, n):
