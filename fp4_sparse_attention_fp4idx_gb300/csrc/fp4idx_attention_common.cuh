@@ -79,6 +79,15 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t c, uint32_t& lo, uint32
   hi = e4m3x2_to_f16x2((uint16_t)(c >> 16));
 }
 
+// 16 bytes read once: not kept in L1.
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // 2^x, flushing results below 2^-126 to zero.
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;

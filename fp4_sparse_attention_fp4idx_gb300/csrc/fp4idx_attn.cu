@@ -19,29 +19,17 @@ int64_t item_rows(int64_t rows, bool sparse) {
   return !sparse && rows >= kTileFrom ? kTileRows : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 }
 
-// Key ranges of an item of the tensor-core kernel, at most: as many as fill
-// the GPU once.
-int64_t tile_splits(int64_t items) { return items < kMaxGrid ? kMaxGrid / items : 1; }
-
 struct Workspace {
   int64_t part_lse, cuts, total;  // offsets in bytes; partial outputs at 0
 };
 
-Workspace workspace_of(int64_t batch, int64_t max_q, int64_t num_heads, int64_t kv_heads,
-                       int64_t head_dim, bool sparse) {
-  const int64_t rows = max_q * (num_heads / kv_heads);
-  const int64_t R = item_rows(rows, sparse);
-  const int64_t items = batch * kv_heads * ((rows + R - 1) / R);
-  int64_t slots = 2 * kMaxGrid, cuts = items * 8;
-  if (R == kTileRows) {
-    const int64_t splits = items > 0 ? tile_splits(items) : 1;
-    slots = splits > 1 ? items * splits : 0;
-    cuts = 0;
-  }
+// Two partial outputs per CTA (an item cut at its share's start and one at
+// its end), and the cut items.
+Workspace workspace_of(int64_t rows, int64_t head_dim) {
   Workspace w;
-  w.part_lse = slots * R * head_dim * 4;
-  w.cuts = w.part_lse + slots * R * 4;
-  w.total = (w.cuts + cuts + 256) / 256 * 256;
+  w.part_lse = 2 * kMaxGrid * rows * head_dim * 4;
+  w.cuts = w.part_lse + 2 * kMaxGrid * rows * 4;
+  w.total = w.cuts + (kMaxGrid * 16 + 255) / 256 * 256;
   return w;
 }
 
@@ -67,8 +55,8 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
       num_tokens >= (1ll << 31) ||
       !workspace_args_ok(items, max_q, num_heads, cache->kv_heads, cache->head_dim))
     return FP4IDX_ERR_SHAPE;
-  const Workspace w = workspace_of(items, max_q, num_heads, cache->kv_heads, cache->head_dim,
-                                   sparse);
+  const int64_t R = item_rows(max_q * (num_heads / cache->kv_heads), sparse);
+  const Workspace w = workspace_of(R, cache->head_dim);
   if (workspace_bytes < (size_t)w.total) return FP4IDX_ERR_SCRATCH;
   if (!dtype_ok(dtype) || !isfinite(softmax_scale)) return FP4IDX_ERR_ARG;
   if (cs != FP4IDX_OK || !aligned(q, 16) || q_token_stride % 8 || q_head_stride % 8 ||
@@ -94,7 +82,7 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
   a.Hq = (int32_t)num_heads;
   a.Hkv = cache->kv_heads;
   a.G = (int32_t)(num_heads / cache->kv_heads);
-  a.R = (int32_t)item_rows(max_q * a.G, sparse);
+  a.R = (int32_t)R;
   a.rc_max = (int32_t)((max_q * a.G + a.R - 1) / a.R);
   a.scale_log2 = softmax_scale * kLog2e;
   a.out = static_cast<uint16_t*>(out);
@@ -102,7 +90,7 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   a.part_out = reinterpret_cast<float*>(ws);
   a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
-  a.cuts = reinterpret_cast<int2*>(ws + w.cuts);
+  a.cuts = reinterpret_cast<int4*>(ws + w.cuts);
   a.err = err_flags;
   return FP4IDX_OK;
 }
@@ -110,16 +98,12 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
 // `max_tiles`: 64-key tiles of an item, at most.
 fp4idx_status launch(AttnArgs& a, int head_dim, bool sparse, int64_t max_tiles, void* stream) {
   const int64_t items = (int64_t)a.batch * a.Hkv * a.rc_max;
-  if (a.R == kTileRows) {
-    const int64_t most = (max_tiles + 7) / 8, splits = tile_splits(items);
-    a.splits = (int32_t)(splits < most ? splits : most);
-    if (items * a.splits >= (1ll << 31)) return FP4IDX_ERR_SHAPE;
-    return launch_tiles(a, head_dim, static_cast<cudaStream_t>(stream));
-  }
   // items of few tiles are not worth cutting: the join costs more than it saves
   a.split = max_tiles > 8;
   const int64_t units = a.split ? items * max_tiles : items;
   const int grid = units < kMaxGrid ? (int)units : kMaxGrid;
+  if (a.R == kTileRows)
+    return launch_tiles(a, head_dim, grid, static_cast<cudaStream_t>(stream));
   return launch_rows(a, head_dim, sparse, grid, static_cast<cudaStream_t>(stream));
 }
 
@@ -132,10 +116,8 @@ extern "C" size_t fp4idx_attention_workspace_bytes(int64_t batch, int64_t max_q,
                                                    int64_t num_heads, int64_t kv_heads,
                                                    int64_t head_dim) {
   if (!workspace_args_ok(batch, max_q, num_heads, kv_heads, head_dim)) return 0;
-  // the larger of the two forms' needs
-  const int64_t dense = workspace_of(batch, max_q, num_heads, kv_heads, head_dim, false).total;
-  const int64_t sparse = workspace_of(batch, max_q, num_heads, kv_heads, head_dim, true).total;
-  return (size_t)(dense > sparse ? dense : sparse);
+  // of the two forms, the dense one's items are never smaller
+  return (size_t)workspace_of(item_rows(max_q * (num_heads / kv_heads), false), head_dim).total;
 }
 
 extern "C" fp4idx_status fp4idx_paged_attention_fp8(

@@ -34,14 +34,15 @@ struct AttnArgs {
   int32_t batch, T, Hq, Hkv, G;
   int32_t R;       // query rows of an item
   int32_t rc_max;  // row chunks of a sequence, at most
-  int32_t splits;  // key ranges of an item (fp4idx_attn_tiles.cu)
   int32_t split;   // items may be cut at tiles (partial outputs in the workspace)
   float scale_log2;
   uint16_t* out;
   float* lse;
   float* part_out;  // [slot][R][D] normalised partial outputs
   float* part_lse;  // [slot][R], log2
-  int2* cuts;       // [batch * Hkv * rc_max]: first CTA and its slot << 16 | CTAs (0: whole)
+  // [kMaxGrid]: the item that begins in a CTA's share and ends in another's:
+  // sequence, row chunk, key head, CTAs * 2 + the first one's slot (0: none)
+  int4* cuts;
   uint32_t* err;
 };
 
@@ -50,7 +51,7 @@ fp4idx_status launch_rows(const AttnArgs& a, int head_dim, bool sparse, int grid
                           cudaStream_t stream);
 
 // Launches the kernel for many rows per item (fp4idx_attn_tiles.cu).
-fp4idx_status launch_tiles(const AttnArgs& a, int head_dim, cudaStream_t stream);
+fp4idx_status launch_tiles(const AttnArgs& a, int head_dim, int grid, cudaStream_t stream);
 
 // Raises a kernel's dynamic shared-memory limit, once per device.
 class SmemOnce {

@@ -423,7 +423,11 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
   int64_t s0, s1;
   Cursor<kSparse> cur;
   const int64_t total = locate_share<kSparse>(a, cur, s0, s1);
-  if (s0 >= s1) return;
+  int4 cut = make_int4(0, 0, 0, 0);
+  if (s0 >= s1) {
+    if (a.split && tid == 0) a.cuts[blockIdx.x] = cut;
+    return;
+  }
 
   Producer<D, kSparse> prod;
   prod.start(a, cur, s0, s1, warp, lane);
@@ -762,39 +766,36 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
       }
       __syncthreads();
     }
-    if (a.split && at == cur.begin && tid == 0) {
-      const int c1 = cta_of(cur.begin + u - 1, total);
-      a.cuts[(int64_t)cur.b * a.Hkv * a.rc_max + cur.it] =
-          make_int2(part, whole ? 0 : c1 - (int)blockIdx.x + 1);
-    }
+    if (!whole && at == cur.begin)  // the first fragment of a cut item
+      cut = make_int4(cur.b, cur.it - head * cur.m.rcs, head,
+                      (cta_of(cur.begin + u - 1, total) - (int)blockIdx.x + 1) * 2 + (part & 1));
     xb = xe;
     at = end;
     if (at < s1) cur.next(a);
   }
+  if (a.split && tid == 0) a.cuts[blockIdx.x] = cut;
   cp_wait<0>();
 }
 
 // Joins the partial outputs of the items that a share's end cut: weights
-// 2^(lse - max lse), in the order of the CTAs.  One block per item, a warp
-// per row.
+// 2^(lse - max lse), in the order of the CTAs.  One block per CTA whose share
+// begins such an item, a warp per row.
 template <int D, bool kSparse>
 __global__ __launch_bounds__(128) void join_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int per = a.Hkv * a.rc_max;
-  const int b = blockIdx.x / per, it = blockIdx.x % per;
-  const Seq m = seq_of<kSparse>(a, b);
-  if (it >= m.items) return;
-  const int2 cut = a.cuts[blockIdx.x];
-  const int n = cut.y;
+  const int cta = blockIdx.x;
+  const int4 cut = a.cuts[cta];
+  const int n = cut.w / 2;
   if (n < 2) return;
-  const int cta = cut.x / 2;
+  const Seq m = seq_of<kSparse>(a, cut.x);
   const int lane = threadIdx.x % 32;
-  const int head = it / m.rcs, row0 = (it - head * m.rcs) * a.R;
+  const int head = cut.z, row0 = cut.y * a.R;
   const int rows = min(m.n * a.G - row0, a.R);
+  const int first = 2 * cta + (cut.w & 1);
   for (int r = threadIdx.x / 32; r < rows; r += 4) {
     float top = -INFINITY;
     for (int f = lane; f < n; f += 32)
-      top = fmaxf(top, a.part_lse[(f == 0 ? cut.x : 2 * (cta + f)) * a.R + r]);
+      top = fmaxf(top, a.part_lse[(f == 0 ? first : 2 * (cta + f)) * a.R + r]);
     for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
     constexpr int kV = D / 32;
     float o[kV], den = 0.0f;
@@ -803,7 +804,7 @@ __global__ __launch_bounds__(128) void join_kernel(const AttnArgs a) {
     if (top != -INFINITY) {
 #pragma unroll 4
       for (int f = 0; f < n; ++f) {
-        const int64_t slot = (int64_t)(f == 0 ? cut.x : 2 * (cta + f)) * a.R + r;
+        const int64_t slot = (int64_t)(f == 0 ? first : 2 * (cta + f)) * a.R + r;
         const float w = exp2_approx(a.part_lse[slot] - top);
         den += w;
         const float* p = a.part_out + slot * D + lane * kV;
@@ -836,8 +837,7 @@ fp4idx_status launch_one(const AttnArgs& a, int grid, cudaStream_t stream) {
   if (launch_kernel(kern, (unsigned)grid, kThreads, bytes, stream, a) != cudaSuccess)
     return FP4IDX_ERR_CUDA;
   if (!a.split) return FP4IDX_OK;
-  return launch_after(join_kernel<D, kSparse>, (unsigned)((int64_t)a.batch * a.Hkv * a.rc_max),
-                      128, stream, a) == cudaSuccess
+  return launch_after(join_kernel<D, kSparse>, (unsigned)grid, 128, stream, a) == cudaSuccess
              ? FP4IDX_OK
              : FP4IDX_ERR_CUDA;
 }

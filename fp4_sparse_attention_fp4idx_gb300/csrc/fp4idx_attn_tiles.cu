@@ -17,21 +17,33 @@
 // the same exponentials, moved by the difference of the two references; a
 // page whose values are 2^60 below M's takes exponentials of its own for l.
 //
-// Roles (13 warps, one CTA per SM).  The item's rows are two M = 128 halves A
-// and B that share every key tile of 128 keys (two pages).
-//   warps 0-3, 4-7  softmax of half A, of half B: a row per thread, its scores
-//                   read from TMEM, its probabilities written back over them
-//   warps 8-11      converters: the codes from global memory through
+// Roles (one CTA per SM).  The item's rows are two M = 128 halves A and B that
+// share every key tile of 128 keys (two pages).
+//   warp 0          issues the MMAs: S = Q K^T, then O += P V with P from
+//                   TMEM.  While half A's softmax runs, half B's products do.
+//                   (One issuer for both keeps the halves out of step; with an
+//                   issuer each they fell into step and 501 us became 643.)
+//   warp 1          walks the CTA's list of work and describes its segments
+//                   and, eight ahead, its tiles: pages, scales, visible rows
+//   warps 4-7       converters: the codes from global memory through
 //                   registers to fp16 tiles in shared memory, keys as
 //                   [key][d], values transposed as [d][key], both K-major in
 //                   128-byte swizzled rows, two stages each; the next tile's
 //                   loads are in flight while this one is converted
-//   warp 12         issues the MMAs: S = Q K^T, then O += P V with P from
-//                   TMEM.  While half A's softmax runs, half B's products do.
-// TMEM: scores A and B at columns 0 and 128 (P over the upper half of its
-// scores, once they are in registers), O at 256 and 256 + D.
+//   warps 8-11, 12-15  softmax of half A, of half B: a row per thread, its
+//                   scores read from TMEM a page at a time, its probabilities
+//                   written back over them.  A register spilled here costs
+//                   much: the shared memory leaves L1 too small to hold it
+//                   (60 bytes of spills a thread: 770 us).
+// TMEM: scores A and B at columns 0 and 128 (P over the first page's scores,
+// once those are in registers), O at 256 and 256 + D.
+// The items and their tiles form one list, cut into equal shares, one per CTA,
+// from the lengths alone; an item cut by a share's end leaves normalised
+// partial outputs, joined by a second kernel in a fixed order.
 // Every wait is bounded (1 s) and a shared abort flag stops every role; MMAs
 // in flight are waited for before TMEM is released.
+
+#include <type_traits>
 
 #include "fp4idx_attn.cuh"
 
@@ -42,10 +54,16 @@ constexpr int kPage = FP4IDX_KV_BLOCK;
 constexpr int kTile = 128;  // keys of a tile
 constexpr int kHalfRows = 128;
 constexpr int kItemRows = 2 * kHalfRows;
-constexpr int kConvWarp = 8, kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
+constexpr int kMmaWarp = 0, kSegWarp = 1, kConvWarp = 4, kSoftWarp = 8;
+constexpr int kSegUsers = 9;       // warps that read a segment: the issuer and the softmax
+constexpr int kThreads = 16 * 32;  // warps 2-3 only complete the warpgroup
+// Registers of a thread, by warpgroup: the launch's 128, moved from the others
+// to the softmax.
+constexpr int kLaunchRegs = 128, kSoftRegs = 144, kConvRegs = 128, kMmaRegs = 96;
+static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs <= 4 * kLaunchRegs, "the launch's registers");
 constexpr int kStages = 2;
-constexpr int kScaleRing = 4;
+constexpr int kTileRing = 8;
+constexpr int kSegRing = 2;
 constexpr float kShift = 10.0f, kSlack = 4.0f, kFar = 60.0f;
 constexpr uint32_t kTmemCols = 512;
 
@@ -56,59 +74,141 @@ __host__ __device__ constexpr uint32_t smem_bytes(int D) {
 }
 
 // One item: 256 consecutive rows (token i, head g: row i * G + g) of a
-// sequence and key head, its keys' tiles [t0, t1) of the visible list.
+// sequence and key head.
 struct Item {
-  int b, head, row0, rows;
+  int row0, rows;
   int q0, first;  // first query token of the sequence, its position
   int hi;         // keys any row sees are below hi
   int ts, tl;     // tiles: 0 .. ts-1, then tl ..
-  int t0, t1;
+  int nt;         // tiles in all, at least one
 };
 
-__device__ __forceinline__ bool item_of(const AttnArgs& a, Item& m) {
-  // the last row chunks first: they see the most keys
-  const int per = a.batch * a.Hkv;
-  const int sp = blockIdx.x % a.splits;
-  const int i = blockIdx.x / a.splits;
-  const int rc = a.rc_max - 1 - i / per;
-  m.b = i % per / a.Hkv;
-  m.head = i % per % a.Hkv;
-  const int ctx = min(max(__ldg(a.ctx + m.b), 0), a.max_context);
+// The rows' chunk rc of sequence b; false: it has no rows.
+__device__ __forceinline__ bool item_of(const AttnArgs& a, int b, int rc, Item& m) {
+  const int ctx = min(max(__ldg(a.ctx + b), 0), a.max_context);
   int full = a.max_q;
-  m.q0 = m.b * a.max_q;
+  m.q0 = b * a.max_q;
   if (a.starts) {
-    m.q0 = __ldg(a.starts + m.b);
-    full = max(__ldg(a.starts + m.b + 1) - m.q0, 0);
+    m.q0 = __ldg(a.starts + b);
+    full = max(__ldg(a.starts + b + 1) - m.q0, 0);
   }
-  const int n = min(full, a.max_q);
   m.first = ctx - full;
   m.row0 = rc * kItemRows;
-  m.rows = min(n * a.G - m.row0, kItemRows);
-  if (m.rows <= 0) return false;
+  m.rows = min(min(full, a.max_q) * a.G - m.row0, kItemRows);
   m.hi = max(min(ctx, m.first + (m.row0 + m.rows - 1) / a.G + 1), 0);
   int lo = a.window > 0 ? max(m.first + m.row0 / a.G - a.window + 1, 0) : 0;
   lo = min(lo, m.hi);
   m.tl = lo / kTile;
   m.ts = a.window > 0 ? min((a.sinks + kTile - 1) / kTile, m.tl) : 0;
-  const int nt = m.ts + (m.hi + kTile - 1) / kTile - m.tl;
-  m.t0 = (int)((int64_t)nt * sp / a.splits);
-  m.t1 = (int)((int64_t)nt * (sp + 1) / a.splits);
-  return true;
+  m.nt = max(m.ts + (m.hi + kTile - 1) / kTile - m.tl, 1);
+  return m.rows > 0;
 }
 
+// The first key of the item's tile t.
 __device__ __forceinline__ int key_of_tile(const Item& m, int t) {
   return (t < m.ts ? t : m.tl + (t - m.ts)) * kTile;
 }
 
-// Waits for a phase; false when another role has given up or after 1 s.
+// The list of work: for each sequence, row chunk and key head the item's
+// tiles.  It is cut into equal shares, one per CTA.
+struct Share {
+  int64_t s0, s1, total;
+  int b, rc, head, off;  // the item of unit s0, and the tile in it
+  int grid;              // CTAs with a share
+};
+
+// A segment of the share: an item's tiles [t0, t1).
+struct Seg {
+  Item m;
+  int b, head, t0, t1;
+  int whole;  // the item as a whole
+  int part;   // else the slot of its partial outputs
+  int more;   // segments follow
+};
+
+// This CTA's share, by the whole CTA.
+__device__ __forceinline__ void locate_share(const AttnArgs& a, Share& sh) {
+  __shared__ int64_t part[kThreads / 32];
+  __shared__ int count[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int64_t pairs = (int64_t)a.batch * a.rc_max;
+  const int64_t each = (pairs + kThreads - 1) / kThreads;
+  const int64_t p0 = min(tid * each, pairs), p1 = min(p0 + each, pairs);
+  int64_t own = 0;
+  int items = 0;
+  Item m;
+  for (int64_t p = p0; p < p1; ++p)
+    if (item_of(a, (int)(p / a.rc_max), (int)(p % a.rc_max), m)) {
+      own += m.nt;
+      ++items;
+    }
+  own *= a.Hkv;
+  int64_t incl = own;
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t o = __shfl_up_sync(kFull, incl, d);
+    if (lane >= d) incl += o;
+  }
+  items = __reduce_add_sync(kFull, items);
+  if (lane == 31) {
+    part[warp] = incl;
+    count[warp] = items;
+  }
+  __syncthreads();
+  int64_t base = 0, total = 0, n = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) base += part[w];
+    total += part[w];
+    n += count[w];
+  }
+  // shares of at least four tiles, but every item may have a CTA of its own
+  const int64_t most = gridDim.x;
+  const int64_t grid = min(max(total / 4, min(n * a.Hkv, most)), most);
+  const int64_t s0 = blockIdx.x < grid ? total * blockIdx.x / grid : 0;
+  const int64_t s1 = blockIdx.x < grid ? total * (blockIdx.x + 1) / grid : 0;
+  const int64_t from = base + incl - own;
+  if (tid == 0) {
+    sh.s0 = s0;
+    sh.s1 = s1;
+    sh.total = total;
+    sh.grid = (int)grid;
+  }
+  if (s0 < s1 && from <= s0 && s0 < from + own) {
+    int64_t at = from;
+    for (int64_t p = p0;; ++p) {
+      const int b = (int)(p / a.rc_max), rc = (int)(p % a.rc_max);
+      if (!item_of(a, b, rc, m)) continue;
+      const int64_t u = (int64_t)m.nt * a.Hkv;
+      if (s0 < at + u) {
+        sh.b = b;
+        sh.rc = rc;
+        sh.head = (int)((s0 - at) / m.nt);
+        sh.off = (int)((s0 - at) % m.nt);
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+}
+
+// The CTA whose share holds unit x.
+__device__ __forceinline__ int cta_of(int64_t x, const Share& sh) {
+  return (int)(((x + 1) * sh.grid - 1) / sh.total);
+}
+
+// Waits for a phase; false when another role has given up or after 1 s.  The
+// clock is read seldom: a read of it costs more than most waits take.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
+  unsigned long long t0 = 0;
   for (;;) {
-    for (int k = 0; k < 16; ++k)
+#pragma unroll 1
+    for (int k = 0; k < 256; ++k)
       if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
+    const unsigned long long now = global_ns();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > kWaitLimitNs) {
       *abort = 1u;
       return false;
     }
@@ -131,30 +231,48 @@ __host__ __device__ constexpr uint32_t f16_idesc(int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kHalfRows >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+// The MMAs and commits take the elected lane as a predicate: the whole warp
+// computes their operands, which then live in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t elected, uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar),
+      "r"(elected)
       : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
 }
 
 __device__ __forceinline__ void fence_before() {
@@ -184,16 +302,40 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+        "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The largest of 32 values, two to an instruction in four chains.
+__device__ __forceinline__ float top32(const float* s) {
+  float x[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int i = 4; i < 28; i += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = max3(x[j], s[i + 2 * j], s[i + 2 * j + 1]);
+  return max3(max3(x[0], s[28], s[29]), max3(x[1], s[30], s[31]), fmaxf(x[2], x[3]));
 }
 
 // (a * b + c, a' * b + c) packed.
@@ -214,12 +356,25 @@ __device__ __forceinline__ float log2_scale(float s) {
 
 __device__ __forceinline__ float or_zero(float m) { return m == -INFINITY ? 0.0f : m; }
 
-// The visible keys of a row in a tile: key i (from the tile's first) with
-// i <= hi and (i >= lo or i < sk).
-struct Vis {
-  int hi, lo, sk;
-  __device__ __forceinline__ bool sees(int i) const { return i <= hi && (i >= lo || i < sk); }
-};
+// Bits i of a word with i <= last.
+__device__ __forceinline__ uint32_t bits_to(int last) {
+  return last >= 31 ? kFull : last < 0 ? 0u : (2u << last) - 1u;
+}
+
+// The keys that a row sees of 32 of a tile's: key i (from the first of the 32)
+// with i <= hi and (i >= lo or i < sk).
+__device__ __forceinline__ uint32_t sees(int hi, int lo, int sk) {
+  return bits_to(hi) & (~bits_to(lo - 1) | bits_to(sk - 1));
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // Barriers.
 enum {
@@ -231,12 +386,37 @@ enum {
   kPFull = kSFull + 2,         // per half: its probabilities are, O rescaled
   kODone = kPFull + 2,         // per half: the product with the values is done
   kQFull = kODone + 2,         // per half: its queries are in shared memory
-  kBars = kQFull + 2
+  kSegFull = kQFull + 2,       // a segment is described
+  kSegEmpty = kSegFull + kSegRing,
+  kTileFull = kSegEmpty + kSegRing,  // a tile is described
+  kTileFree = kTileFull + kTileRing,  // and nothing reads that any more
+  kBars = kTileFree + kTileRing
+};
+
+// The arrivals that complete a barrier's phase.
+__device__ __forceinline__ int arrivals(int i) {
+  if (i >= kTileFull) return 1;
+  if (i >= kSegEmpty) return kSegUsers;
+  if (i >= kSegFull) return 1;
+  const bool commit = (i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kPFull) ||
+                      (i >= kODone && i < kQFull);
+  return commit ? 1 : 4;
+}
+
+// A tile of the CTA's list, described ahead of its use.
+struct alignas(16) TileInfo {
+  float scale[4];  // ks of its two pages, vs of both (negative: page left out)
+  int64_t off[2];  // bytes from the codes' start to each page's rows of the head
+  int key0;        // its first key
+  int rows[2];     // rows of the pages that hold visible keys
+  int last;        // no tile follows
 };
 
 struct Ctl {
   uint64_t bars[kBars];
-  float4 scales[kScaleRing];  // ks of the tile's two pages, vs of both (vs < 0: page left out)
+  TileInfo tiles[kTileRing];
+  Share share;
+  Seg segs[kSegRing];
   uint32_t tmem;
   uint32_t abort;
 };
@@ -253,17 +433,15 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
   volatile uint32_t* abort = &ctl.abort;
   const auto bar = [&](int i) { return smem_addr(&ctl.bars[i]); };
 
-  Item m;
-  if (!item_of(a, m)) return;
-  const int nt = m.t1 - m.t0;
-  const int halves = m.rows > kHalfRows ? 2 : 1;
+  locate_share(a, ctl.share);
+  const Share& share = ctl.share;
+  if (share.s0 >= share.s1) {
+    if (tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
 
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) {
-      const bool commit = (i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kPFull) ||
-                          (i >= kODone && i < kQFull);
-      mbar_init(bar(i), commit ? 1 : 4);
-    }
+    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), arrivals(i));
     fence_mbar_init();
     ctl.abort = 0;
   }
@@ -277,26 +455,43 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = ctl.tmem;
+  const uint32_t tmem = __shfl_sync(kFull, ctl.tmem, 0);
 
-  if (warp < kConvWarp) {
+  if (warp >= kSoftWarp) {
     // ------------------------------------------------------------- softmax
-    const int half = warp / 4;
-    if (half < halves) {
-      const int r = m.row0 + half * kHalfRows + tid % kHalfRows;  // row of the sequence
-      const int rl = tid % kHalfRows;
+    set_regs_up<kSoftRegs>();
+    const int half = (warp - kSoftWarp) / 4, rl = tid % kHalfRows;
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t ts = tmem + lanes + half * 128;
+    const uint32_t to = tmem + lanes + 256 + half * D;
+    uint32_t n = 0, n_half = 0;  // tiles so far: of the CTA, of this half
+    bool ok = true;
+    for (uint32_t i = 0; ok; ++i) {
+      ok = __all_sync(kFull, wait_bar(bar(kSegFull + i % kSegRing), i / kSegRing & 1u, abort));
+      if (!ok) break;
+      const Seg& seg = ctl.segs[i % kSegRing];
+      const Item& m = seg.m;
+      const int nt = seg.t1 - seg.t0;
+      const bool more = seg.more != 0;
+      if (half == 1 && m.rows <= kHalfRows) {  // no rows in this half
+        n += nt;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSegEmpty + i % kSegRing));
+        if (!more) break;
+        continue;
+      }
+      const bool whole = seg.whole != 0;
+      const int part = seg.part;
+      const int r = m.row0 + half * kHalfRows + rl;  // row of the sequence
       const bool live_row = r < m.row0 + m.rows;
-      const int tok = m.q0 + r / a.G, h = m.head * a.G + r % a.G;
+      const int tok = m.q0 + r / a.G, h = seg.head * a.G + r % a.G;
       const bool live = live_row && tok >= 0 && tok < a.T;
-      const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
-      const uint32_t ts = tmem + lanes + half * 128, tp = ts + 64;
-      const uint32_t to = tmem + lanes + 256 + half * D;
       // ---- this row of Q, scaled by a power of two, into shared memory
       float fac;
       {
         const uint16_t* src = a.q + (live ? tok * a.q_ts + h * a.q_hs : 0);
         float amax = 0.0f;
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           uint4 w = make_uint4(0, 0, 0, 0);
           if (live) w = __ldg(reinterpret_cast<const uint4*>(src) + c);
@@ -315,7 +510,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
           up = -up;
         }
         const uint32_t dst = sq + half * kHalves * kQHalf + rl * 128;
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           uint4 w = make_uint4(0, 0, 0, 0);
           if (live) w = __ldg(reinterpret_cast<const uint4*>(src) + c);
@@ -340,51 +535,45 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
       const int pos_lo = m.first + w0 / a.G;
       const int pos_hi = m.first + min(w0 + 31, m.row0 + m.rows - 1) / a.G;
       const bool idle = w0 >= m.row0 + m.rows;  // no row: keep the barriers going
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kSegEmpty + i % kSegRing));
       float mm = -INFINITY, MM = -INFINITY, l = 0.0f;
-      bool ok = true;
-      for (int t = 0; t < nt; ++t) {
-        ok = __all_sync(kFull, wait_bar(bar(kSFull + half), t & 1, abort));
+      const int lo_key = a.window > 0 ? pos - a.window + 1 : -(1 << 30);
+      for (int t = 0; t < nt; ++t, ++n, ++n_half) {
+        ok = __all_sync(kFull, wait_bar(bar(kSFull + half), n_half & 1, abort));
         if (!ok) break;
         fence_after();
         if (!idle) {
-          const float4 sc = ctl.scales[t % kScaleRing];
-          const int kb = key_of_tile(m, m.t0 + t);
-          const bool both = sc.z >= 0.0f && sc.w >= 0.0f;
-          const bool full = both && kb + kTile <= pos_lo + 1 &&
+          const TileInfo& info = ctl.tiles[n % kTileRing];
+          const float4 sc = lds_f4(smem_addr(info.scale));
+          int kb;
+          asm volatile("ld.shared.s32 %0, [%1];" : "=r"(kb) : "r"(smem_addr(&info.key0)));
+          const bool full = fminf(sc.z, sc.w) >= 0.0f && kb + kTile <= pos_lo + 1 &&
                             (a.window <= 0 || kb > pos_hi - a.window || kb + kTile <= a.sinks);
-          const Vis vis{pos - kb, a.window > 0 ? pos - kb - a.window + 1 : -(1 << 30),
-                        a.sinks - kb};
-          const float c0 = fac * sc.x, c1 = fac * sc.y;
+          // a factor of zero would make a masked score NaN
+          const float c0 = fmaxf(fac * sc.x, 0x1p-100f), c1 = fmaxf(fac * sc.y, 0x1p-100f);
           const float e0 = log2_scale(sc.z), e1 = log2_scale(sc.w);
-          float s[64];
-          const auto mask = [&](int from, bool page) {
+          float s[kPage];  // one page's scores at a time
+          const auto load = [&](int page) {
+            tmem_ld32(ts + page * kPage, s);
+            tmem_ld32(ts + page * kPage + 32, s + 32);
+            tmem_wait_ld();
+            if (!full) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (!page || !vis.sees(from + i)) s[i] = -INFINITY;
-          };
-          const auto top = [&]() {
-            float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+              for (int w = 0; w < 2; ++w) {
+                const int from = kb + page * kPage + w * 32;
+                uint32_t on = sees(pos - from, lo_key - from, a.sinks - from);
+                if ((page ? sc.w : sc.z) < 0.0f) on = 0;
 #pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-              x0 = fmaxf(x0, s[i]);
-              x1 = fmaxf(x1, s[i + 1]);
-              x2 = fmaxf(x2, s[i + 2]);
-              x3 = fmaxf(x3, s[i + 3]);
+                for (int e = 0; e < 32; ++e)
+                  if (!(on >> e & 1u)) s[w * 32 + e] = -INFINITY;
+              }
             }
-            return fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
           };
-          // a masked maximum times a factor of zero stays masked
-          const auto times = [](float x, float c) { return x == -INFINITY ? x : x * c; };
-          tmem_ld32(ts, s);
-          tmem_ld32(ts + 32, s + 32);
-          tmem_wait_ld();
-          if (!full) mask(0, sc.z >= 0.0f);
-          const float x0 = times(top(), c0);
-          tmem_ld32(ts + 64, s);
-          tmem_ld32(ts + 96, s + 32);
-          tmem_wait_ld();
-          if (!full) mask(64, sc.w >= 0.0f);
-          const float x1 = times(top(), c1);
+          load(1);
+          const float x1 = fmaxf(top32(s), top32(s + 32)) * c1;
+          load(0);
+          const float x0 = fmaxf(top32(s), top32(s + 32)) * c0;
           const float m1 = fmaxf(mm, fmaxf(x0, x1));
           const float M1 = fmaxf(x0 + e0, x1 + e1);
           // ---- O's reference, moved seldom
@@ -393,60 +582,59 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
             const float al = move ? exp2_approx(MM - M1) : 1.0f;
             if (move) MM = M1;
             if (t > 0) {
-              ok = __all_sync(kFull, wait_bar(bar(kODone + half), (t - 1) & 1, abort));
+              ok = __all_sync(kFull, wait_bar(bar(kODone + half), (n_half - 1) & 1, abort));
               if (!ok) break;
               fence_after();
-              // a register's worth of columns at a time: s stays live
+              // few columns at a time: s stays in registers
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(to + c, o);
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(to + c, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= al;
-                tmem_st32(to + c, reinterpret_cast<const uint32_t*>(o));
+                for (int i = 0; i < 16; ++i) o[i] *= al;
+                tmem_st16(to + c, reinterpret_cast<const uint32_t*>(o));
               }
-              tmem_wait_st();
             }
           }
           const float mz = or_zero(m1), Mz = or_zero(MM);
           l *= exp2_approx(mm - mz);
           mm = m1;
-          const auto weigh = [&](float c, float e, uint32_t col) {
-            const float ref = Mz - e - kShift;
+#pragma unroll
+          for (int page = 0; page < 2; ++page) {
+            const float c = page ? c1 : c0;
+            const float ref = Mz - (page ? e1 : e0) - kShift;
+            if (page) load(1);
             const bool far = ref + kShift - mz > kFar;
-            float a0 = 0.0f, a1 = 0.0f;
-            if (__any_sync(kFull, far)) {
+            const bool any_far = __any_sync(kFull, far);
+            float own = 0.0f, b0 = 0.0f, b1 = 0.0f, b2 = 0.0f, b3 = 0.0f;
 #pragma unroll
-              for (int i = 0; i < 64; ++i)
-                a0 += s[i] == -INFINITY ? 0.0f : exp2_approx(fmaf(s[i], c, -mz));
-            }
-            uint32_t p[32];
-            float b0 = 0.0f, b1 = 0.0f;
+            for (int w = 0; w < 2; ++w) {
+              const float* v = s + w * 32;
+              if (any_far) {
 #pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              float y0, y1;
-              fma2s(y0, y1, s[i], s[i + 1], c, -ref);
-              if (!full) {  // -inf * 0
-                y0 = s[i] == -INFINITY ? -INFINITY : y0;
-                y1 = s[i + 1] == -INFINITY ? -INFINITY : y1;
+                for (int q = 0; q < 32; ++q) own += exp2_approx(fmaf(v[q], c, -mz));
               }
-              y0 = exp2_approx(y0);
-              y1 = exp2_approx(y1);
-              b0 += y0;
-              b1 += y1;
-              p[i / 2] = pack16<true>(y0, y1);
+              uint32_t p[16];
+#pragma unroll
+              for (int q = 0; q < 32; q += 4) {
+                float y0, y1, y2, y3;
+                fma2s(y0, y1, v[q], v[q + 1], c, -ref);
+                fma2s(y2, y3, v[q + 2], v[q + 3], c, -ref);
+                y0 = exp2_approx(y0);
+                y1 = exp2_approx(y1);
+                y2 = exp2_approx(y2);
+                y3 = exp2_approx(y3);
+                sum2(b0, b1, b0, b1, y0, y1);
+                sum2(b2, b3, b2, b3, y2, y3);
+                p[q / 2] = pack16<true>(y0, y1);
+                p[q / 2 + 1] = pack16<true>(y2, y3);
+              }
+              tmem_st16(ts + page * 32 + w * 16, p);
             }
-            tmem_st32(col, p);
-            a1 = (b0 + b1) * exp2_approx(ref - mz);
-            l += far ? a0 : a1;
-          };
-          weigh(c1, e1, tp + 32);
-          tmem_ld32(ts, s);
-          tmem_ld32(ts + 32, s + 32);
-          tmem_wait_ld();
-          if (!full) mask(0, sc.z >= 0.0f);
-          weigh(c0, e0, tp);
+            const float moved = (b0 + b1 + (b2 + b3)) * exp2_approx(ref - mz);
+            l += far ? own : moved;
+          }
           tmem_wait_st();
         }
         fence_before();
@@ -454,7 +642,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
         if (lane == 0) mbar_arrive(bar(kPFull + half));
       }
       // ---- the output row
-      if (ok && nt > 0) ok = __all_sync(kFull, wait_bar(bar(kODone + half), (nt - 1) & 1, abort));
+      if (ok) ok = __all_sync(kFull, wait_bar(bar(kODone + half), (n_half - 1) & 1, abort));
       if (ok && !idle) {
         fence_after();
         const bool some = mm != -INFINITY;
@@ -462,19 +650,17 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
         const float f = some ? exp2_approx(MM - mm - kShift) : 0.0f;
         const float lse2 = some ? mm + __log2f(l) : -INFINITY;
         const int64_t orow = (int64_t)tok * a.Hq + h;
-        const int64_t prow = (int64_t)blockIdx.x * kItemRows + half * kHalfRows + rl;
+        const int64_t prow = (int64_t)part * kItemRows + half * kHalfRows + rl;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           __syncwarp();
-          if (nt > 0) {
-            tmem_ld32(to + c, o);
-            tmem_wait_ld();
-          }
+          tmem_ld32(to + c, o);
+          tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * inv * f : 0.0f;
           if (!live) {
-          } else if (a.splits > 1) {
+          } else if (!whole) {
             float4* dst = reinterpret_cast<float4*>(a.part_out + prow * D + c);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -490,205 +676,291 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
           }
         }
         if (live) {
-          if (a.splits > 1)
+          if (!whole)
             a.part_lse[prow] = lse2;
           else if (a.lse)
             a.lse[orow] = lse2 * kLn2;
         }
       }
+      if (!more) break;
     }
-  } else if (warp < kMmaWarp) {
+  } else if (warp >= kConvWarp) {
     // ---------------------------------------------------------- converters
+    set_regs_down<kConvRegs>();
     const int cw = warp - kConvWarp;
-    const int32_t* table = a.table + m.b * a.tstride;
-    constexpr int kRowLanes = D / 16;              // 16-byte pieces of a row of codes
-    constexpr int kKRows = 32 / kRowLanes;         // key rows of one warp load
-    constexpr int kKLoads = kTile / (4 * kKRows);  // key loads of a lane and tile
-    // values: a warp step covers 64 keys (16 lanes x 4 rows) x 32 d (2 lanes)
-    constexpr int kVSteps = (kTile / 64) * (D / 32) / 4;
-    uint4 kreg[kKLoads], vreg[kVSteps][4];
-    int page0 = -1, page1 = -1;  // of the tile whose loads come next
-
-    const auto pages = [&](int t) {
-      page0 = page1 = -1;
-      if (t >= nt) return;
-      const int kb = key_of_tile(m, m.t0 + t);
-      if (kb < m.hi) page0 = __ldg(table + kb / kPage);
-      if (kb + kPage < m.hi) page1 = __ldg(table + kb / kPage + 1);
-    };
-    const auto page_ok = [&](int p) { return p >= 0 && p < a.num_blocks; };
-    const auto load_k = [&](int t) {
-      const int kb = key_of_tile(m, m.t0 + t);
+    // the tile whose codes are loaded next
+    int64_t off[2];
+    int rows[2];
+    bool last = false;
+    const auto look = [&](uint32_t n) {
+      const bool ok = 0 != __all_sync(kFull, wait_bar(bar(kTileFull + n % kTileRing),
+                                                      n / kTileRing & 1u, abort));
+      const TileInfo& info = ctl.tiles[n % kTileRing];
+      last = info.last != 0;
 #pragma unroll
-      for (int i = 0; i < kKLoads; ++i) {
-        const int key = (cw * kKLoads + i) * kKRows + lane / kRowLanes;
-        const int p = key < kPage ? page0 : page1;
+      for (int k = 0; k < 2; ++k) {
+        off[k] = info.off[k];
+        rows[k] = ok ? info.rows[k] : 0;
+      }
+      return ok;
+    };
+    // Keys: a row of codes is kRowLanes lanes of 16 bytes; load i of a lane is
+    // row key + 4 * kRows * i.
+    constexpr int kRowLanes = D / 16, kRows = 32 / kRowLanes, kLoads = kTile / (4 * kRows);
+    const int key = cw * kRows + lane / kRowLanes;
+    const int c = lane % kRowLanes;  // d 16c .. 16c + 15
+    uint4 kreg[kLoads];
+    const auto load_k = [&]() {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int k = i / (kLoads / 2), row = key + i % (kLoads / 2) * (4 * kRows);
         kreg[i] = make_uint4(0, 0, 0, 0);
-        if (page_ok(p) && kb + key < m.hi)
-          kreg[i] = __ldg(reinterpret_cast<const uint4*>(
-              a.kc + p * a.cstride + ((int64_t)m.head * kPage + key % kPage) * D +
-              lane % kRowLanes * 16));
+        if (row < rows[k]) kreg[i] = ld_stream(a.kc + off[k] + row * D + c * 16);
       }
     };
-    const auto load_v = [&](int t, int p0, int p1) {
-      const int kb = key_of_tile(m, m.t0 + t);
+    // the lanes of the second column block store their upper half first: the
+    // two blocks lie on the same banks
+    const int flip = c / 4;
+    const uint32_t atk = sk + c / 4 * (kTile * 128) + key * 128;
+    const uint32_t at0 = atk + ((c % 4 * 2 + flip) ^ (key & 7)) * 16;
+    const uint32_t at1 = atk + ((c % 4 * 2 + 1 - flip) ^ (key & 7)) * 16;
+    // Values: a step covers a page's 64 keys (16 lanes x 4 rows) and 32 d (2
+    // lanes x 16).
+    constexpr int kSteps = D / 64;
+    const int d0 = (D == 128 ? cw : cw % 2) * 32 + lane / 16 * 16;
+    const int q = lane % 16;  // keys 4q .. 4q + 3: 8 bytes of a row of d
+    uint4 vreg[kSteps][4];
+    const auto page_of = [&](int i) { return D == 128 ? i : cw / 2; };
+    const auto load_v = [&]() {
 #pragma unroll
-      for (int i = 0; i < kVSteps; ++i) {
-        const int step = cw * kVSteps + i;
-        const int kh = step / (D / 32), d = step % (D / 32) * 32 + lane / 16 * 16;
-        const int p = kh == 0 ? p0 : p1;
+      for (int i = 0; i < kSteps; ++i) {
+        const uint8_t* src = a.vc + (page_of(i) ? off[1] : off[0]) + q * 4 * D + d0;
+        const int n = (page_of(i) ? rows[1] : rows[0]) - q * 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int key = lane % 16 * 4 + j;
           vreg[i][j] = make_uint4(0, 0, 0, 0);
-          if (page_ok(p) && kb + kh * kPage + key < m.hi)
-            vreg[i][j] = __ldg(reinterpret_cast<const uint4*>(
-                a.vc + p * a.cstride + ((int64_t)m.head * kPage + key) * D + d));
+          if (j < n) vreg[i][j] = ld_stream(src + j * D);
         }
       }
     };
-    pages(0);
-    if (nt > 0) load_k(0);
-    bool ok = true;
-    for (int t = 0; t < nt; ++t) {
-      const int stage = t % kStages;
-      const uint32_t parity = (uint32_t)(t / kStages + 1) & 1u;
-      const int p0 = page0, p1 = page1;
-      load_v(t, p0, p1);
-      pages(t + 1);
-      // ---- keys: [key][d]
-      if (t >= kStages) ok = __all_sync(kFull, wait_bar(bar(kKEmpty + stage), parity, abort));
+    const uint32_t atv = sv + d0 * 128 + q / 2 * 16 + q % 2 * 8;
+
+    bool ok = look(0);
+    load_k();
+    for (uint32_t n = 0; ok; ++n) {
+      const int stage = n % kStages;
+      const bool done = last;
+      load_v();
+      if (n >= kStages)
+        ok = __all_sync(kFull, wait_bar(bar(kKEmpty + stage), (n / kStages + 1) & 1u, abort));
       if (!ok) break;
-      if (cw == 0 && lane == 0) {
-        const int kb = key_of_tile(m, m.t0 + t);
-        float4 sc = make_float4(1.0f, 1.0f, -1.0f, -1.0f);
-        if (page_ok(p0)) {
-          sc.x = a.ks[p0 * a.sstride + m.head];
-          sc.z = fabsf(a.vs[p0 * a.sstride + m.head]);
-        } else if (kb < m.hi) {
-          flag_error(a.err, FP4IDX_ERRFLAG_PAGE);
-        }
-        if (page_ok(p1)) {
-          sc.y = a.ks[p1 * a.sstride + m.head];
-          sc.w = fabsf(a.vs[p1 * a.sstride + m.head]);
-        } else if (kb + kPage < m.hi) {
-          flag_error(a.err, FP4IDX_ERRFLAG_PAGE);
-        }
-        ctl.scales[t % kScaleRing] = sc;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const uint32_t u[4] = {kreg[i].x, kreg[i].y, kreg[i].z, kreg[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e4m3x4_to_f16x2(u[j], o[2 * j], o[2 * j + 1]);
+        const uint32_t to = stage * kv_bytes(D) + i * (4 * kRows * 128);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at0 + to),
+                     "r"(flip ? o[4] : o[0]), "r"(flip ? o[5] : o[1]), "r"(flip ? o[6] : o[2]),
+                     "r"(flip ? o[7] : o[3])
+                     : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at1 + to),
+                     "r"(flip ? o[0] : o[4]), "r"(flip ? o[1] : o[5]), "r"(flip ? o[2] : o[6]),
+                     "r"(flip ? o[3] : o[7])
+                     : "memory");
       }
-      {
-        const uint32_t dst = sk + stage * kv_bytes(D);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kKFull + stage));
+      if (!done) {
+        ok = look(n + 1);
+        load_k();
+      }
+      if (ok && n >= kStages)
+        ok = __all_sync(kFull, wait_bar(bar(kVEmpty + stage), (n / kStages + 1) & 1u, abort));
+      if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < kKLoads; ++i) {
-          const int key = (cw * kKLoads + i) * kKRows + lane / kRowLanes;
-          const int c = lane % kRowLanes;  // d 16c .. 16c + 15
-          const uint32_t u[4] = {kreg[i].x, kreg[i].y, kreg[i].z, kreg[i].w};
-          uint32_t o[8];
+      for (int i = 0; i < kSteps; ++i) {
+        const uint32_t blk = atv + stage * kv_bytes(D) + page_of(i) * (D * 128);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) e4m3x4_to_f16x2(u[j], o[2 * j], o[2 * j + 1]);
-          const uint32_t row = dst + c / 4 * (kTile * 128) + key * 128;
-          // the lanes of the second column block store their upper half first:
-          // the two blocks lie on the same banks
-          const int flip = c / 4;
+        for (int e = 0; e < 4; ++e) {  // d0 + 4e ..
+          const uint32_t r0 = (&vreg[i][0].x)[e], r1 = (&vreg[i][1].x)[e];
+          const uint32_t r2 = (&vreg[i][2].x)[e], r3 = (&vreg[i][3].x)[e];
+          // byte pairs (key 0, key 1) and (2, 3) of four d
+          uint32_t lo[4], hi[4];
+          e4m3x4_to_f16x2(prmt(r0, r1, 0x5140u), lo[0], lo[1]);
+          e4m3x4_to_f16x2(prmt(r0, r1, 0x7362u), lo[2], lo[3]);
+          e4m3x4_to_f16x2(prmt(r2, r3, 0x5140u), hi[0], hi[1]);
+          e4m3x4_to_f16x2(prmt(r2, r3, 0x7362u), hi[2], hi[3]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int w = e ^ flip;
-            const uint32_t at = row + (((c % 4) * 2 + w) ^ (key & 7)) * 16;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at),
-                         "r"(w ? o[4] : o[0]), "r"(w ? o[5] : o[1]), "r"(w ? o[6] : o[2]),
-                         "r"(w ? o[7] : o[3])
+          for (int j = 0; j < 4; ++j) {
+            const int d = 4 * e + j;  // of the swizzle: d0 is a multiple of 16
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"((blk ^ (d % 8 * 16)) + d * 128),
+                         "r"(lo[j]), "r"(hi[j])
                          : "memory");
           }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kKFull + stage));
       }
-      if (t + 1 < nt) load_k(t + 1);
-      // ---- values: [d][key]
-      if (t >= kStages) ok = __all_sync(kFull, wait_bar(bar(kVEmpty + stage), parity, abort));
-      if (!ok) break;
-      {
-        const uint32_t dst = sv + stage * kv_bytes(D);
-#pragma unroll
-        for (int i = 0; i < kVSteps; ++i) {
-          const int step = cw * kVSteps + i;
-          const int kh = step / (D / 32), d0 = step % (D / 32) * 32 + lane / 16 * 16;
-          const uint32_t blk = dst + kh * (D * 128);
-          const int q = lane % 16;  // keys 4q .. 4q + 3: 8 bytes of a row
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {  // d0 + 4c ..
-            const uint32_t r0 = (&vreg[i][0].x)[c], r1 = (&vreg[i][1].x)[c];
-            const uint32_t r2 = (&vreg[i][2].x)[c], r3 = (&vreg[i][3].x)[c];
-            // byte pairs (key 0, key 1) and (2, 3) of four d
-            const uint32_t a01 = prmt(r0, r1, 0x5140u), a23 = prmt(r0, r1, 0x7362u);
-            const uint32_t b01 = prmt(r2, r3, 0x5140u), b23 = prmt(r2, r3, 0x7362u);
-            uint32_t lo[4], hi[4];
-            e4m3x4_to_f16x2(a01, lo[0], lo[1]);
-            e4m3x4_to_f16x2(a23, lo[2], lo[3]);
-            e4m3x4_to_f16x2(b01, hi[0], hi[1]);
-            e4m3x4_to_f16x2(b23, hi[2], hi[3]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int d = d0 + 4 * c + j;
-              const uint32_t at = blk + d * 128 + (((q / 2) ^ (d & 7)) * 16) + (q % 2) * 8;
-              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(lo[j]), "r"(hi[j])
-                           : "memory");
-            }
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kVFull + stage));
-      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kVFull + stage));
+      if (done) break;
     }
-  } else if (lane == 0 && nt > 0) {
+  } else {
+    set_regs_down<kMmaRegs>();
+  }
+  if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer
     constexpr uint32_t kQkDesc = f16_idesc(kTile), kPvDesc = f16_idesc(D);
+    // a descriptor's address field moves by (bytes >> 4)
+    const uint64_t dq = sw128_desc(sq), dk = sw128_desc(sk), dv = sw128_desc(sv);
+    const uint32_t elected = elect_one();
     const auto issue_s = [&](int half, int stage) {
-      const uint32_t qa = sq + half * kHalves * kQHalf, kb = sk + stage * kv_bytes(D);
+      const uint64_t qa = dq + half * (kHalves * kQHalf >> 4), kb = dk + stage * (kv_bytes(D) >> 4);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k % 4) * 32;
-        mma_ss(tmem + half * 128, sw128_desc(qa + k / 4 * kQHalf + off),
-               sw128_desc(kb + k / 4 * (kTile * 128) + off), kQkDesc, k > 0);
-      }
-      mma_commit(bar(kSFull + half));
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(elected, tmem + half * 128, qa + (k / 4 * (kQHalf >> 4) + k % 4 * 2),
+               kb + (k / 4 * (kTile * 128 >> 4) + k % 4 * 2), kQkDesc, k > 0);
+      mma_commit(elected, bar(kSFull + half));
     };
     const auto issue_o = [&](int half, int stage, bool first) {
-      const uint32_t vb = sv + stage * kv_bytes(D);
+      const uint64_t vb = dv + stage * (kv_bytes(D) >> 4);
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
-        mma_ts(tmem + 256 + half * D, tmem + half * 128 + 64 + k * 8,
-               sw128_desc(vb + k / 4 * (D * 128) + (k % 4) * 32), kPvDesc, !first || k > 0);
-      mma_commit(bar(kODone + half));
+        mma_ts(elected, tmem + 256 + half * D, tmem + half * 128 + k * 8,
+               vb + (k / 4 * (D * 128 >> 4) + k % 4 * 2), kPvDesc, !first || k > 0);
+      mma_commit(elected, bar(kODone + half));
     };
-    bool ok = wait_bar(bar(kKFull), 0, abort);
-    for (int h = 0; h < halves && ok; ++h) {
-      ok = wait_bar(bar(kQFull + h), 0, abort);
+    const auto release = [&](int i) { mma_commit(elected, bar(i)); };
+    const auto wait = [&](int i, uint32_t parity) {
+      return __all_sync(kFull, wait_bar(bar(i), parity, abort)) != 0;
+    };
+    bool ok = true;
+    uint32_t n = 0, n_a = 0, n_b = 0;  // tiles so far: of the CTA, of each half
+    uint32_t q_a = 0, q_b = 0;         // segments so far, of each half
+    for (uint32_t i = 0; ok; ++i) {
+      ok = wait(kSegFull + i % kSegRing, i / kSegRing & 1u);
       if (!ok) break;
-      fence_after();
-      issue_s(h, 0);
-    }
-    if (ok) mma_commit(bar(kKEmpty));
-    for (int t = 0; t < nt && ok; ++t) {
-      const int stage = t % kStages, next = (t + 1) % kStages;
-      ok = wait_bar(bar(kVFull + stage), (uint32_t)(t / kStages) & 1u, abort);
+      const Seg& seg = ctl.segs[i % kSegRing];
+      const int nt = seg.t1 - seg.t0;
+      const int halves = seg.m.rows > kHalfRows ? 2 : 1;
+      const bool more = seg.more != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kSegEmpty + i % kSegRing));
+      ok = wait(kKFull + n % kStages, n / kStages & 1u);
       for (int h = 0; h < halves && ok; ++h) {
-        ok = wait_bar(bar(kPFull + h), t & 1, abort);
+        ok = wait(kQFull + h, (h ? q_b : q_a) & 1u);
         if (!ok) break;
         fence_after();
-        issue_o(h, stage, t == 0);
-        if (t + 1 < nt) {
-          if (h == 0) ok = wait_bar(bar(kKFull + next), (uint32_t)((t + 1) / kStages) & 1u, abort);
+        issue_s(h, n % kStages);
+      }
+      ++q_a;
+      q_b += halves - 1;
+      if (ok) release(kKEmpty + n % kStages);
+      for (int t = 0; t < nt && ok; ++t, ++n) {
+        const int stage = n % kStages, next = (n + 1) % kStages;
+        ok = wait(kVFull + stage, n / kStages & 1u);
+        for (int h = 0; h < halves && ok; ++h) {
+          ok = wait(kPFull + h, (h ? n_b : n_a) & 1u);
           if (!ok) break;
-          issue_s(h, next);
+          fence_after();
+          issue_o(h, stage, t == 0);
+          if (t + 1 < nt) {
+            if (h == 0) ok = wait(kKFull + next, (n + 1) / kStages & 1u);
+            if (!ok) break;
+            issue_s(h, next);
+          }
+        }
+        if (!ok) break;
+        // both halves have their probabilities, and V is converted
+        if (lane == 0) mbar_arrive(bar(kTileFree + n % kTileRing));
+        ++n_a;
+        n_b += halves - 1;
+        release(kVEmpty + stage);
+        if (t + 1 < nt) release(kKEmpty + next);
+      }
+      if (!more) break;
+    }
+  } else if (warp == kSegWarp) {
+    // ------------------------------------------------------ work list
+    int b = share.b, rc = share.rc, head = share.head, t0 = share.off;
+    int64_t at = share.s0;
+    int4 cut = make_int4(0, 0, 0, 0);
+    uint32_t n = 0;  // tiles described
+    for (uint32_t i = 0; at < share.s1; ++i) {
+      if (i >= kSegRing &&
+          !__all_sync(kFull, wait_bar(bar(kSegEmpty + i % kSegRing), (i / kSegRing + 1) & 1u,
+                                      abort)))
+        break;
+      Seg sg;
+      item_of(a, b, rc, sg.m);
+      sg.b = b;
+      sg.head = head;
+      sg.t0 = t0;
+      sg.t1 = (int)min((int64_t)sg.m.nt, t0 + (share.s1 - at));
+      sg.whole = t0 == 0 && sg.t1 == sg.m.nt;
+      sg.part = 2 * blockIdx.x + (t0 == 0 && i > 0 ? 1 : 0);
+      if (!sg.whole && t0 == 0)  // the first fragment of a cut item
+        cut = make_int4(b, rc, head,
+                        (cta_of(at + sg.m.nt - 1, share) - (int)blockIdx.x + 1) * 2 +
+                            (sg.part & 1));
+      at += sg.t1 - t0;
+      sg.more = at < share.s1;
+      if (lane == 0) {
+        ctl.segs[i % kSegRing] = sg;
+        mbar_arrive(bar(kSegFull + i % kSegRing));
+      }
+      // its tiles, four at a time, a lane each
+      bool ok = true;
+      for (int t = sg.t0; t < sg.t1 && ok; t += 4) {
+        const int k = min(sg.t1 - t, 4);
+        TileInfo info;
+        if (lane < k) {
+          info.key0 = key_of_tile(sg.m, t + lane);
+          info.last = !sg.more && t + lane + 1 == sg.t1;
+          const int32_t* row = a.table + b * a.tstride + info.key0 / kPage;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            info.rows[e] = min(max(sg.m.hi - info.key0 - e * kPage, 0), kPage);
+            int page = info.rows[e] > 0 ? __ldg(row + e) : -1;
+            info.scale[e] = 1.0f;
+            info.scale[2 + e] = -1.0f;
+            if (page >= 0 && page < a.num_blocks) {
+              info.scale[e] = a.ks[page * a.sstride + head];
+              info.scale[2 + e] = fabsf(a.vs[page * a.sstride + head]);
+            } else {
+              if (info.rows[e] > 0) flag_error(a.err, FP4IDX_ERRFLAG_PAGE);
+              info.rows[e] = page = 0;
+            }
+            info.off[e] = page * a.cstride + (int64_t)head * kPage * D;
+          }
+        }
+        for (int e = 0; e < k && ok; ++e, ++n) {
+          if (n >= kTileRing)
+            ok = __all_sync(kFull, wait_bar(bar(kTileFree + n % kTileRing),
+                                            (n / kTileRing + 1) & 1u, abort));
+          if (ok && lane == e) {
+            ctl.tiles[n % kTileRing] = info;
+            mbar_arrive(bar(kTileFull + n % kTileRing));
+          }
+          __syncwarp();
         }
       }
       if (!ok) break;
-      mma_commit(bar(kVEmpty + stage));
-      if (t + 1 < nt) mma_commit(bar(kKEmpty + next));
+      t0 = 0;
+      if (++head == a.Hkv && sg.more) {
+        head = 0;
+        Item it;
+        do {
+          if (++rc == a.rc_max) {
+            rc = 0;
+            ++b;
+          }
+        } while (!item_of(a, b, rc, it));
+      }
     }
+    if (lane == 0) a.cuts[blockIdx.x] = cut;
   }
 
   __syncwarp();
@@ -702,7 +974,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
       asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(b) : "memory");
       mbar_init(b, 1);
       fence_mbar_init();
-      mma_commit(b);
+      mma_commit(1, b);
       mbar_wait_bounded(b, 0);
     }
     __syncthreads();
@@ -716,63 +988,62 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
   }
 }
 
-// Joins the partial outputs of an item's key ranges: weights 2^(lse - max),
-// in order.  A warp per row; grid: items (without the ranges) x 8 rows.
+// Joins the partial outputs of the items that a share's end cut: weights
+// 2^(lse - max), in the order of the CTAs.  Blocks (CTA whose share begins the
+// item, 32 of its rows), four rows a warp.
 template <int D>
 __global__ __launch_bounds__(256) void join_tiles_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kBlocks = kItemRows / 8;
-  const int i = blockIdx.x / kBlocks;
-  const int rl = blockIdx.x % kBlocks * 8 + threadIdx.x / 32;
+  constexpr int kBlocks = kItemRows / 32;
+  const int cta = blockIdx.x / kBlocks;
+  const int4 cut = a.cuts[cta];
+  const int n = cut.w / 2;
+  if (n < 2) return;
+  Item m;
+  item_of(a, cut.x, cut.y, m);
   const int lane = threadIdx.x % 32;
-  const int per = a.batch * a.Hkv;
-  const int rc = a.rc_max - 1 - i / per, b = i % per / a.Hkv, head = i % per % a.Hkv;
-  int q0 = b * a.max_q, n = a.max_q;
-  if (a.starts) {
-    q0 = __ldg(a.starts + b);
-    n = min(max(__ldg(a.starts + b + 1) - q0, 0), a.max_q);
-  }
-  const int r = rc * kItemRows + rl;
-  const int tok = q0 + r / a.G;
-  if (r >= n * a.G || tok < 0 || tok >= a.T) return;
-  float top = -INFINITY;
-  for (int s = 0; s < a.splits; ++s)
-    top = fmaxf(top, a.part_lse[((int64_t)i * a.splits + s) * kItemRows + rl]);
+  const auto slot = [&](int f) { return (int64_t)2 * (cta + f) + (f == 0 ? cut.w & 1 : 0); };
   constexpr int kV = D / 32;
-  float o[kV], den = 0.0f;
+  for (int k = 0; k < 4; ++k) {
+    const int rl = blockIdx.x % kBlocks * 32 + threadIdx.x / 32 * 4 + k;
+    const int r = m.row0 + rl;
+    const int tok = m.q0 + r / a.G;
+    if (rl >= m.rows || tok < 0 || tok >= a.T) continue;
+    float top = -INFINITY;
+    for (int f = 0; f < n; ++f) top = fmaxf(top, a.part_lse[slot(f) * kItemRows + rl]);
+    float o[kV], den = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kV; ++j) o[j] = 0.0f;
-  if (top != -INFINITY) {
+    for (int j = 0; j < kV; ++j) o[j] = 0.0f;
+    if (top != -INFINITY) {
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-      const int64_t row = ((int64_t)i * a.splits + s) * kItemRows + rl;
-      const float w = exp2_approx(a.part_lse[row] - top);
-      den += w;
+      for (int f = 0; f < n; ++f) {
+        const int64_t row = slot(f) * kItemRows + rl;
+        const float w = exp2_approx(a.part_lse[row] - top);
+        den += w;
 #pragma unroll
-      for (int j = 0; j < kV; ++j) o[j] = fmaf(a.part_out[row * D + lane * kV + j], w, o[j]);
+        for (int j = 0; j < kV; ++j) o[j] = fmaf(a.part_out[row * D + lane * kV + j], w, o[j]);
+      }
+      const float inv = __frcp_rn(den);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) o[j] *= inv;
     }
-    const float inv = __frcp_rn(den);
+    const int64_t orow = (int64_t)tok * a.Hq + cut.z * a.G + r % a.G;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * kV);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) o[j] *= inv;
+    for (int j = 0; j < kV; j += 2) dst[j / 2] = pack16(a.half, o[j], o[j + 1]);
+    if (a.lse && lane == 0)
+      a.lse[orow] = top == -INFINITY ? -INFINITY : (top + __log2f(den)) * kLn2;
   }
-  const int64_t orow = (int64_t)tok * a.Hq + head * a.G + r % a.G;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * kV);
-#pragma unroll
-  for (int j = 0; j < kV; j += 2) dst[j / 2] = pack16(a.half, o[j], o[j + 1]);
-  if (a.lse && lane == 0)
-    a.lse[orow] = top == -INFINITY ? -INFINITY : (top + __log2f(den)) * kLn2;
 }
 
 template <int D>
-fp4idx_status launch_d(const AttnArgs& a, cudaStream_t stream) {
+fp4idx_status launch_d(const AttnArgs& a, int grid, cudaStream_t stream) {
   static SmemOnce once;
   if (!once.set(tiles_kernel<D>, smem_bytes(D))) return FP4IDX_ERR_CUDA;
-  const int64_t items = (int64_t)a.batch * a.Hkv * a.rc_max;
-  if (launch_kernel(tiles_kernel<D>, (unsigned)(items * a.splits), kThreads, smem_bytes(D), stream,
-                    a) != cudaSuccess)
+  if (launch_kernel(tiles_kernel<D>, (unsigned)grid, kThreads, smem_bytes(D), stream, a) !=
+      cudaSuccess)
     return FP4IDX_ERR_CUDA;
-  if (a.splits == 1) return FP4IDX_OK;
-  return launch_after(join_tiles_kernel<D>, (unsigned)(items * (kItemRows / 8)), 256, stream, a) ==
+  return launch_after(join_tiles_kernel<D>, (unsigned)(grid * (kItemRows / 32)), 256, stream, a) ==
                  cudaSuccess
              ? FP4IDX_OK
              : FP4IDX_ERR_CUDA;
@@ -780,8 +1051,8 @@ fp4idx_status launch_d(const AttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-fp4idx_status launch_tiles(const AttnArgs& a, int head_dim, cudaStream_t stream) {
-  return head_dim == 128 ? launch_d<128>(a, stream) : launch_d<64>(a, stream);
+fp4idx_status launch_tiles(const AttnArgs& a, int head_dim, int grid, cudaStream_t stream) {
+  return head_dim == 128 ? launch_d<128>(a, grid, stream) : launch_d<64>(a, grid, stream);
 }
 
 }  // namespace fp4idx_impl
