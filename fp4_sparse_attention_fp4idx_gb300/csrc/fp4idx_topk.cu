@@ -4,7 +4,7 @@
 //
 // A logit becomes an unsigned key that orders like the float (0 for what can
 // never be selected).  One CTA per row, bound by reading the row once:
-//   1. 2,048 samples of the row give a threshold that about k + 4 sigma of
+//   1. 4,096 samples of the row give a threshold that about k + 4 sigma of
 //      its entries reach;
 //   2. one pass over the row keeps the entries that reach it (a few
 //      thousand) with their places, in shared memory;
@@ -17,6 +17,15 @@
 // more entries than fit reach the threshold (rows with many equal logits, or
 // laid out against the samples), the row is selected by the general method,
 // four histogram passes of 8 bits over the row and an ordered one.
+//
+// The steps but the second are chains of short phases between barriers, so
+// what counts is how many rows an SM works on at once: the candidates stay in
+// shared memory rather than in registers, four CTAs of 512 threads to an SM.
+// Few long rows are given a cluster of eight CTAs each: all of them find the
+// threshold, each filters an eighth of the row, and the first one's shared
+// memory collects the candidates.
+
+#include <float.h>
 
 #include "fp4idx_attn.cuh"
 
@@ -25,11 +34,13 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPer = 12;                      // candidates a thread holds
-constexpr int kCap = kThreads * kPer;         // 6144 candidates
-constexpr int kSamples = 4 * kThreads;
-constexpr int kBins = 2048;                   // 11 bits
-constexpr int kMaxMapCols = 1 << 18;          // two bit maps of 32 KB
+constexpr int kBins = 2048;           // 11 bits
+constexpr int kMaxMapCols = 1 << 18;  // a bit map of 32 KB
+constexpr int kCluster = 8;
+
+// Candidates that fit.  The threshold lets through k + 4 sigma of the sampled
+// rank: about 1.6 k at k = 2048 of 65,536.
+constexpr int cap_of(int k) { return k <= 1024 ? 3072 : k * 9 / 4; }
 
 struct TopkArgs {
   const float* logits;
@@ -39,7 +50,8 @@ struct TopkArgs {
   int64_t istride;
   int32_t* counts;
   int32_t cols, k;
-  int32_t map_words;  // words of a bit map; 0: columns beyond kMaxMapCols
+  int32_t map_words;  // words of the bit map; 0: columns beyond kMaxMapCols
+  int32_t cap;        // candidates that fit
 };
 
 // Orders like x; 0 for -inf and NaN; -0 as +0.
@@ -54,14 +66,18 @@ __device__ __forceinline__ float float_of(uint32_t key) {  // key != 0
 }
 
 struct Shared {
-  uint32_t bins[kBins];
-  uint32_t part[kWarps];
+  uint32_t bins[kBins];  // histograms; afterwards the bit map of equal keys
+  uint32_t part[kWarps + 1];
   uint32_t part2[kWarps];
   uint32_t found[4];
+  uint32_t lo, hi;   // least and largest key
+  uint32_t few[32];  // the keys of a bin of few
   uint32_t count;
 };
 
-// Exclusive prefix sum over the block, and the sum of all.
+// Exclusive prefix sum over the block, and the sum of all.  (Every instruction
+// that all threads execute costs an SM with four CTAs 16 cycles, so the first
+// warp alone sums over the warps.)
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint32_t& all) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   uint32_t incl = v;
@@ -72,22 +88,59 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint3
   }
   if (lane == 31) part[warp] = incl;
   __syncthreads();
-  uint32_t base = 0;
-  all = 0;
+  if (warp == 0) {
+    const uint32_t own = lane < kWarps ? part[lane] : 0u;
+    uint32_t sum = own;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base += part[w];
-    all += part[w];
+    for (int d = 1; d < kWarps; d *= 2) {
+      const uint32_t o = __shfl_up_sync(kFull, sum, d);
+      if (lane >= d) sum += o;
+    }
+    if (lane < kWarps) part[lane] = sum - own;
+    if (lane == kWarps - 1) part[kWarps] = sum;
   }
   __syncthreads();
-  return base + incl - v;
+  all = part[kWarps];
+  return part[warp] + incl - v;
+}
+
+// Of the bins' counts: the bin that holds the want-th largest (found[0]), the
+// number above it (found[1]) and in it (found[2]).
+__device__ __forceinline__ void find_bin(uint32_t want, Shared& sh) {
+  const int tid = threadIdx.x;
+  // thread t sums the bins from the top: 4t .. 4t + 3 counted downwards
+  constexpr int kEach = kBins / kThreads;
+  uint32_t c[kEach], own = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    c[i] = sh.bins[kBins - 1 - (tid * kEach + i)];
+    own += c[i];
+  }
+  uint32_t all;
+  uint32_t above = block_scan(own, sh.part, all);
+  if (above < want && above + own >= want) {
+    int i = 0;
+#pragma unroll
+    for (; i < kEach - 1; ++i) {
+      if (above + c[i] >= want) break;
+      above += c[i];
+    }
+    uint32_t n = c[0];
+#pragma unroll
+    for (int j = 1; j < kEach; ++j) n = i == j ? c[j] : n;
+    sh.found[0] = (uint32_t)(kBins - 1 - (tid * kEach + i));
+    sh.found[1] = above;
+    sh.found[2] = n;
+  }
+  __syncthreads();
 }
 
 // Narrows [lo, hi] to where the want-th largest key lies, by at most `passes`
 // histograms; keys outside [lo, hi] do not count.  On return the keys > hi
 // are all selected and `want` of those in [lo, hi] are; `in` is their number.
-template <int N>
-__device__ __forceinline__ void narrow(const uint32_t (&key)[N], uint32_t& lo, uint32_t& hi,
+// each(f): calls f for each of the thread's keys.
+template <typename Each>
+__device__ __forceinline__ void narrow(const Each& each, uint32_t& lo, uint32_t& hi,
                                        uint32_t& want, uint32_t& in, int passes, Shared& sh) {
   const int tid = threadIdx.x;
   for (int p = 0; p < passes && lo < hi && in != want; ++p) {
@@ -96,41 +149,45 @@ __device__ __forceinline__ void narrow(const uint32_t (&key)[N], uint32_t& lo, u
 #pragma unroll
     for (int i = 0; i < kBins / kThreads; ++i) sh.bins[tid + i * kThreads] = 0;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (key[i] >= lo && key[i] <= hi) atomicAdd(&sh.bins[(key[i] - lo) >> shift], 1u);
+    each([&](uint32_t key) {
+      if (key >= lo && key <= hi) atomicAdd(&sh.bins[(key - lo) >> shift], 1u);
+    });
     __syncthreads();
-    // thread t sums the bins from the top: 4t .. 4t + 3 counted downwards
-    constexpr int kEach = kBins / kThreads;
-    uint32_t c[kEach], own = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      c[i] = sh.bins[kBins - 1 - (tid * kEach + i)];
-      own += c[i];
-    }
-    uint32_t all;
-    uint32_t above = block_scan(own, sh.part, all);
-    if (above < want && above + own >= want) {
-      int i = 0;
-#pragma unroll
-      for (; i < kEach - 1; ++i) {
-        if (above + c[i] >= want) break;
-        above += c[i];
-      }
-      uint32_t n = c[0];
-#pragma unroll
-      for (int j = 1; j < kEach; ++j) n = i == j ? c[j] : n;
-      sh.found[0] = (uint32_t)(kBins - 1 - (tid * kEach + i));
-      sh.found[1] = above;
-      sh.found[2] = n;
-    }
-    __syncthreads();
+    find_bin(want, sh);
     const uint32_t bin = sh.found[0];
     want -= sh.found[1];
     in = sh.found[2];
     lo += bin << shift;
     const uint32_t top = lo + ((1u << shift) - 1u);
     hi = top < hi && top >= lo ? top : hi;
+    if (in <= 32 && in != want && lo < hi) {  // few: ranked by one warp
+      if (tid == 0) sh.found[3] = 0;
+      if (tid < 32) sh.few[tid] = 0;
+      __syncthreads();
+      each([&](uint32_t key) {
+        if (key >= lo && key <= hi) sh.few[atomicAdd(&sh.found[3], 1u)] = key;
+      });
+      __syncthreads();
+      if (tid < 32) {
+        const uint32_t own = sh.few[tid];
+        uint32_t above = 0, same = 0;
+#pragma unroll 8
+        for (int l = 0; l < 32; ++l) {
+          const uint32_t o = __shfl_sync(kFull, own, l);
+          above += o > own;
+          same += o == own;
+        }
+        if (own != 0 && above < want && above + same >= want) {
+          sh.found[0] = own;
+          sh.found[1] = above;
+          sh.found[2] = same;
+        }
+      }
+      __syncthreads();
+      lo = hi = sh.found[0];
+      want -= sh.found[1];
+      in = sh.found[2];
+    }
     __syncthreads();
   }
 }
@@ -219,177 +276,248 @@ __device__ __noinline__ void select_general(const TopkArgs& a, const float* x, i
   if (tid == 0 && a.counts) a.counts[row] = (int32_t)done;
 }
 
-__global__ __launch_bounds__(kThreads, 3) void topk_kernel(const TopkArgs a) {
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// The address of the first CTA's copy of a shared-memory word.
+__device__ __forceinline__ uint32_t in_first(const void* p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(p)));
+  return a;
+}
+
+// Appends the places of the entries of x[from, from + n) that reach thr to a
+// list of the CTA, *count of them so far.  What does not fit is counted only.
+// A lane takes 16 entries at a time: a bit for each, one prefix sum over the
+// warp, and a loop over the few that are set.
+__device__ __forceinline__ void filter(const float* x, int from, int n, float thr,
+                                       uint32_t* places, uint32_t* count, uint32_t cap) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  x += from;
+  const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) / 4 % 4), n);
+  const int nv = (n - head) / 4;
+  const float4* xv = reinterpret_cast<const float4*>(x + head);
+  const auto append = [&](uint32_t hits, const auto& place_of) {
+    const uint32_t own = __popc(hits);
+    uint32_t incl = own;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const uint32_t o = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += o;
+    }
+    uint32_t at = 0;
+    if (lane == 31 && incl != 0) at = atomicAdd(count, incl);
+    at = __shfl_sync(kFull, at, 31) + incl - own;
+    for (; hits != 0; hits &= hits - 1, ++at)
+      if (at < cap) places[at] = (uint32_t)place_of(__ffs((int)hits) - 1);
+  };
+  constexpr int kLoads = 4;
+  for (int base = warp * 32 * kLoads; base < nv; base += kThreads * kLoads) {
+    float4 w[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int e = base + i * 32 + lane;
+      w[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (e < nv) w[i] = __ldg(xv + e);
+    }
+    uint32_t hits = 0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (w[i].x >= thr) hits |= 1u << (4 * i);
+      if (w[i].y >= thr) hits |= 2u << (4 * i);
+      if (w[i].z >= thr) hits |= 4u << (4 * i);
+      if (w[i].w >= thr) hits |= 8u << (4 * i);
+    }
+    const int first = from + head + (base + lane) * 4;
+    append(hits, [&](int b) { return first + b / 4 * 128 + b % 4; });
+  }
+  if (warp == 0) {  // the ends that are not on 16-byte words: at most 3 + 3
+    const int rest = head + nv * 4;
+    const int e = lane < head ? lane : rest + lane - head;
+    const bool hit = e < n && (lane < head || e >= rest) && __ldg(x + e) >= thr;
+    append(hit, [&](int) { return from + e; });
+  }
+}
+
+template <bool kClustered>
+__global__ __launch_bounds__(kThreads, kClustered ? 1 : 4) void topk_kernel(const TopkArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
   uint32_t* const ckey = reinterpret_cast<uint32_t*>(smem);  // candidates
-  uint32_t* const cidx = ckey + kCap;
-  uint32_t* const map = cidx + kCap;  // selected places
-  uint32_t* const tie = map + a.map_words;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int64_t row = blockIdx.x;
+  uint32_t* const cidx = ckey + a.cap;
+  uint32_t* const map = cidx + a.cap;  // selected places
+  const int tid = threadIdx.x, lane = tid % 32;
+  const int64_t row = kClustered ? blockIdx.x / kCluster : blockIdx.x;
+  const uint32_t rank = kClustered ? cluster_rank() : 0;
   const float* x = a.logits + row * a.stride;
   int32_t* out = a.indices + row * a.istride;
   int n = a.lens ? a.lens[row] : a.cols;
   n = n < 0 ? 0 : n > a.cols ? a.cols : n;
-  if (a.map_words == 0) return select_general(a, x, n, out, row, sh);
-  const int words = (n + 31) / 32;
-  for (int i = tid; i < words; i += kThreads) map[i] = tie[i] = 0;
-
-  uint32_t key[kPer];
-  uint32_t top = 0, low = 1, total;
-  const bool direct = n <= kCap;
-  if (direct) {  // every entry is a candidate, in place
-    uint32_t valid = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid + i * kThreads;
-      key[i] = e < n ? key_of(__ldg(x + e)) : 0u;
-      valid += key[i] != 0;
-      top = max(top, key[i]);
-    }
-    valid = __reduce_add_sync(kFull, valid);
-    top = __reduce_max_sync(kFull, top);
-    if (lane == 0) {
-      sh.part[warp] = valid;
-      sh.part2[warp] = top;
-    }
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      total += sh.part[w];
-      top = max(top, sh.part2[w]);
-    }
-    __syncthreads();
-  } else {
-    // ---- the threshold: the sample of rank k/n * samples + 4 sigma
-    float thr = -INFINITY;
-    {
-      uint32_t s[4];
-      uint32_t smin = kFull, smax = 0;
-      const int64_t g = (int64_t)(tid / 2) * (n - 8) / (kThreads / 2 - 1) + (tid % 2) * 4;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[i] = key_of(__ldg(x + g + i));
-        smax = max(smax, s[i]);
-        smin = min(smin, s[i] ? s[i] : kFull);
-      }
-      smax = __reduce_max_sync(kFull, smax);
-      smin = __reduce_min_sync(kFull, smin);
-      if (lane == 0) {
-        sh.part[warp] = smax;
-        sh.part2[warp] = smin;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        smax = max(smax, sh.part[w]);
-        smin = min(smin, sh.part2[w]);
-      }
-      if (tid == 0) sh.count = 0;
-      __syncthreads();
-      const float p = (float)a.k / (float)n;
-      uint32_t want = (uint32_t)(p * kSamples + 4.0f * sqrtf(p * (1.0f - p) * kSamples)) + 4u;
-      // more samples wanted than there are (k near n, or few that count): all
-      if (p < 1.0f && want < kSamples && smax != 0) {
-        uint32_t in = kFull;
-        narrow(s, smin, smax, want, in, 2, sh);
-        if (smin != 0) thr = float_of(smin);
-      }
-    }
-    // ---- what reaches it, with its place
-    const auto keep = [&](float v, int e) {
-      const bool hit = v >= thr && v > -INFINITY;
-      const uint32_t m = __ballot_sync(kFull, hit);
-      if (m == 0) return;
-      uint32_t at = 0;
-      if (lane == 0) at = atomicAdd(&sh.count, (uint32_t)__popc(m));
-      at = __shfl_sync(kFull, at, 0) + __popc(m & ((1u << lane) - 1u));
-      if (hit && at < kCap) {
-        ckey[at] = key_of(v);
-        cidx[at] = (uint32_t)e;
-      }
-    };
+  if (!kClustered && a.map_words == 0) return select_general(a, x, n, out, row, sh);
+  // the row starts on its way to L2 while its samples are looked at
+  if (rank == 0 && n > a.cap && tid < 32) {
+    constexpr int kPiece = 4096;  // entries
     const int head = (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) / 4 % 4);
-    const int nv = (n - head) / 4;
-    const float4* xv = reinterpret_cast<const float4*>(x + head);
-    constexpr int kLoads = 4;
-    for (int base = 0; base < nv; base += kThreads * kLoads) {
-      float4 v[kLoads];
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int e = base + i * kThreads + tid;
-        v[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (e < nv) v[i] = __ldg(xv + e);
-      }
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int e = head + (base + i * kThreads + tid) * 4;
-        const bool h0 = v[i].x >= thr && v[i].x > -INFINITY;
-        const bool h1 = v[i].y >= thr && v[i].y > -INFINITY;
-        const bool h2 = v[i].z >= thr && v[i].z > -INFINITY;
-        const bool h3 = v[i].w >= thr && v[i].w > -INFINITY;
-        const uint32_t m0 = __ballot_sync(kFull, h0), m1 = __ballot_sync(kFull, h1);
-        const uint32_t m2 = __ballot_sync(kFull, h2), m3 = __ballot_sync(kFull, h3);
-        const uint32_t c0 = __popc(m0), c1 = __popc(m1), c2 = __popc(m2), c3 = __popc(m3);
-        const uint32_t c = c0 + c1 + c2 + c3;
-        if (c == 0) continue;
-        uint32_t at = 0;
-        if (lane == 0) at = atomicAdd(&sh.count, c);
-        at = __shfl_sync(kFull, at, 0);
-        const uint32_t below = (1u << lane) - 1u;
-        const auto put = [&](bool h, uint32_t m, uint32_t first, float f, int place) {
-          const uint32_t slot = first + __popc(m & below);
-          if (h && slot < kCap) {
-            ckey[slot] = key_of(f);
-            cidx[slot] = (uint32_t)place;
-          }
-        };
-        put(h0, m0, at, v[i].x, e);
-        put(h1, m1, at + c0, v[i].y, e + 1);
-        put(h2, m2, at + c0 + c1, v[i].z, e + 2);
-        put(h3, m3, at + c0 + c1 + c2, v[i].w, e + 3);
-      }
-    }
-    if (warp == 0) {  // the row's ends, not on 16-byte words: at most 3 + 3
-      const int rest = head + nv * 4;
-      const int e = lane < head ? lane : rest + lane - head;
-      const bool on = lane < head || (lane >= head && e < n);
-      keep(on ? __ldg(x + e) : -INFINITY, e);
-    }
-    __syncthreads();
-    total = sh.count;
-    // below k: the threshold was too high, unless it was none at all
-    if (total > kCap || (total < (uint32_t)a.k && thr != -INFINITY))
-      return select_general(a, x, n, out, row, sh);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t e = tid + i * kThreads;
-      key[i] = e < total ? ckey[e] : 0u;
-      top = max(top, key[i]);
-    }
-    top = __reduce_max_sync(kFull, top);
-    if (lane == 0) sh.part[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = max(top, sh.part[w]);
-    __syncthreads();
-    if (thr != -INFINITY) low = key_of(thr);
+    for (int at = head + lane * kPiece; at + 4 <= n; at += 32 * kPiece)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x + at),
+                   "r"(min(kPiece, (n - at) / 4 * 4) * 4)
+                   : "memory");
   }
+  const int words = (n + 31) / 32;
+  for (int i = tid; i < words; i += kThreads) map[i] = 0;
+  if (tid == 0) sh.count = 0;
+
+  float thr = -FLT_MAX;  // what reaches it can be selected: neither NaN nor -inf
+  if (tid == 0) {
+    sh.lo = kFull;
+    sh.hi = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kBins / kThreads; ++i) sh.bins[tid + i * kThreads] = 0;
+  __syncthreads();
+  if (n > a.cap) {
+    // ---- the threshold: the sample of rank k/n * samples + 4 sigma.  Groups
+    // of 8 neighbours, a lane four of them: a load that meets 32 lines holds
+    // the L1 for as many cycles.
+    const bool twice = n > 65536;
+    const int samples = twice ? 8 * kThreads : 4 * kThreads;
+    const int head = (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) / 4 % 4);
+    const float4* xv = reinterpret_cast<const float4*>(x + head);
+    const int groups = (n - head) / 4 - 1;  // a group may begin at any of these words
+    uint32_t s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i == 1 && !twice) break;
+      const int g = i * (kThreads / 2) + tid / 2, of = samples / 8;
+      const float4 w = __ldg(xv + (int)((int64_t)g * groups / of) + tid % 2);
+      s[4 * i] = key_of(w.x);
+      s[4 * i + 1] = key_of(w.y);
+      s[4 * i + 2] = key_of(w.z);
+      s[4 * i + 3] = key_of(w.w);
+    }
+    uint32_t smin = kFull, smax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      smax = max(smax, s[i]);
+      smin = min(smin, s[i] ? s[i] : kFull);
+    }
+    smax = __reduce_max_sync(kFull, smax);
+    smin = __reduce_min_sync(kFull, smin);
+    if (lane == 0) {
+      atomicMax(&sh.hi, smax);
+      atomicMin(&sh.lo, smin);
+    }
+    __syncthreads();
+    smax = sh.hi;
+    smin = sh.lo;
+    const float p = (float)a.k / (float)n;
+    uint32_t want = (uint32_t)(p * samples + 4.0f * sqrtf(p * (1.0f - p) * samples)) + 4u;
+    // more samples wanted than there are (few entries that count): all
+    if (p < 1.0f && want < (uint32_t)samples && smax != 0) {
+      uint32_t in = kFull;
+      // by value, in equal steps: keys crowd into few bins, and lanes that
+      // meet in a bin take turns
+      const float lo = float_of(smin), step = (float_of(smax) - lo) * (1.0f / kBins);
+      if (step > 0.0f && step < INFINITY) {
+        const float inv = __frcp_rn(step);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (s[i])
+            atomicAdd(&sh.bins[min((uint32_t)((float_of(s[i]) - lo) * inv), kBins - 1u)], 1u);
+        __syncthreads();
+        find_bin(want, sh);
+        in = sh.found[2];
+        thr = fmaf((float)sh.found[0], step, lo);  // near the bin's lower end: near is enough
+        __syncthreads();
+      }
+      if (in > 64) {  // the values lie too far apart for equal steps
+        narrow(
+            [&](const auto& f) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) f(s[i]);
+            },
+            smin, smax, want, in, 2, sh);
+        thr = float_of(smin);
+      }
+    }
+  }
+  __syncthreads();
+  // ---- what reaches it, with its place
+  if constexpr (kClustered) {
+    const int slice = ((n + kCluster - 1) / kCluster + 3) / 4 * 4;
+    const int from = min((int)rank * slice, n);
+    filter(x, from, min(slice, n - from), thr, cidx, &sh.count, (uint32_t)a.cap);
+    __syncthreads();
+    const uint32_t own = sh.count;
+    cluster_sync();  // every CTA has its count, and no other's is added to it yet
+    if (rank != 0) {  // behind the first CTA's own
+      if (tid == 0) {
+        uint32_t at;
+        asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+                     : "=r"(at)
+                     : "r"(in_first(&sh.count)), "r"(own)
+                     : "memory");
+        sh.found[0] = at;
+      }
+      __syncthreads();
+      const uint32_t at = sh.found[0];
+      const uint32_t i0 = in_first(cidx);
+      for (uint32_t e = tid; e < min(own, (uint32_t)a.cap); e += kThreads)
+        if (at + e < (uint32_t)a.cap)
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(i0 + (at + e) * 4), "r"(cidx[e])
+                       : "memory");
+    }
+    cluster_sync();  // the first CTA has them all
+    if (rank != 0) return;
+  } else {
+    filter(x, 0, n, thr, cidx, &sh.count, (uint32_t)a.cap);
+    __syncthreads();
+  }
+  const uint32_t total = sh.count;
+  // below k: the threshold was too high, unless it was none at all
+  if (total > (uint32_t)a.cap || (total < (uint32_t)a.k && thr != -FLT_MAX))
+    return select_general(a, x, n, out, row, sh);
 
   // ---- the k-th largest: keys above `hi` are selected, and `want` of those
   // in [low, hi]
-  uint32_t want = (uint32_t)a.k, in = total, hi = top;
+  uint32_t want = (uint32_t)a.k, in = total, low = 1, hi = 0;
   const bool all = total <= (uint32_t)a.k;
-  if (!all) narrow(key, low, hi, want, in, 4, sh);
+  if (!all) {
+    low = key_of(thr);
+    for (uint32_t e = tid; e < total; e += kThreads) {
+      const uint32_t key = key_of(__ldg(x + cidx[e]));
+      ckey[e] = key;
+      hi = max(hi, key);
+    }
+    hi = __reduce_max_sync(kFull, hi);
+    if (lane == 0) atomicMax(&sh.hi, hi);
+    __syncthreads();
+    hi = sh.hi;
+    narrow(
+        [&](const auto& f) {
+          for (uint32_t e = tid; e < total; e += kThreads) f(ckey[e]);
+        },
+        low, hi, want, in, 4, sh);
+  }
   const bool limited = !all && in != want;  // then low == hi: equal keys
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (key[i] == 0 || (!all && key[i] < low)) continue;
-    const uint32_t e = direct ? tid + i * kThreads : cidx[tid + i * kThreads];
-    uint32_t* const m = limited && key[i] <= hi ? tie : map;
-    atomicOr(m + e / 32, 1u << (e % 32));
+  // their bit map takes the histograms' place, where that is large enough
+  uint32_t* const tie = a.map_words <= kBins ? sh.bins : map + a.map_words;
+  if (limited) {
+    for (int w = tid; w < words; w += kThreads) tie[w] = 0;
+    __syncthreads();
+  }
+  for (uint32_t e = tid; e < total; e += kThreads) {
+    if (!all && ckey[e] < low) continue;
+    uint32_t* const m = limited && ckey[e] <= hi ? tie : map;
+    atomicOr(m + cidx[e] / 32, 1u << (cidx[e] % 32));
   }
   __syncthreads();
   // ---- the bit map in order; thread t owns words [w0, w1)
@@ -433,17 +561,34 @@ extern "C" fp4idx_status fp4idx_topk_tokens(const float* logits, int64_t logits_
   if (!aligned(logits, 4) || !aligned(row_lens, 4) || !aligned(indices, 4) || !aligned(counts, 4))
     return FP4IDX_ERR_ALIGN;
   TopkArgs a = {logits, logits_stride, row_lens, indices, indices_stride, counts,
-                (int32_t)num_cols, (int32_t)k, 0};
+                (int32_t)num_cols, (int32_t)k, 0, 0};
+  a.cap = cap_of(a.k);
   size_t bytes = 0;
+  bool clustered = false;
   if (num_cols <= kMaxMapCols) {
     a.map_words = (int32_t)((num_cols + 31) / 32);
     if (a.map_words == 0) a.map_words = 1;
-    bytes = 2 * (kCap + (size_t)a.map_words) * 4;
-    static SmemOnce once;
-    if (!once.set(topk_kernel, 2 * (kCap + kMaxMapCols / 32) * 4)) return FP4IDX_ERR_CUDA;
+    bytes = (2 * (size_t)a.cap + (a.map_words <= kBins ? 1 : 2) * a.map_words) * 4;
+    constexpr int most = (2 * cap_of(4096) + 2 * kMaxMapCols / 32) * 4;
+    static SmemOnce once, once_clustered;
+    if (!once.set(topk_kernel<false>, most) || !once_clustered.set(topk_kernel<true>, most))
+      return FP4IDX_ERR_CUDA;
+    // a cluster per row where the rows leave most SMs idle and are long
+    // enough for an eighth to be worth its own CTA
+    clustered = num_rows * kCluster <= kMaxGrid && num_cols >= 16384;
   }
-  return launch_kernel(topk_kernel, (unsigned)num_rows, kThreads, bytes,
-                       static_cast<cudaStream_t>(stream), a) == cudaSuccess
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clustered ? num_rows * kCluster : num_rows));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {kCluster, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = clustered ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, clustered ? topk_kernel<true> : topk_kernel<false>, a) ==
+                 cudaSuccess
              ? FP4IDX_OK
              : FP4IDX_ERR_CUDA;
 }

@@ -90,6 +90,29 @@ def test_many_rows_and_a_long_row():
     check(torch.sort(torch.randn(2, 70001, generator=g, device="cuda")).values, 2048)
 
 
+@pytest.mark.parametrize("rows", [1, 19, 20])
+@pytest.mark.parametrize("kind", ["plain", "equal", "ties", "holes", "outliers", "falling"])
+def test_long_rows_on_both_sides_of_the_cluster_rule(rows, kind):
+    """Up to 19 rows are filtered by a cluster each; ragged lengths, some too
+    short for every CTA of the cluster to have a share."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    lens = torch.tensor([[70003, 0, 3, 25, 3071, 3073, 40000][i % 7] for i in range(rows)],
+                        dtype=torch.int32, device="cuda")
+    big = make(kind, rows, 70006, g)
+    check(big[:, 1:70004], 1000, lens)
+
+
+def test_wide_maps_and_many_ties():
+    """More columns than the histograms' memory holds a bit map for."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    x = torch.randn(25, 140003, generator=g, device="cuda")
+    x[:, ::50] = 3.0  # 2,801 equal ones near the border
+    check(x, 2048)
+    check(x[:3], 2048)
+
+
 def test_empty():
     ind, cnt = F().topk_tokens(torch.empty(3, 0, device="cuda"), 8)
     assert bool((ind == -1).all()) and bool((cnt == 0).all())
