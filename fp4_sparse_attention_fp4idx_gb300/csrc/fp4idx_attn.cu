@@ -15,8 +15,9 @@ constexpr int64_t kTileFrom = 128;
 constexpr int64_t kTileRows = 256;
 
 // Query rows of an item; selected tokens never take the tensor-core kernel.
-int64_t item_rows(int64_t rows, bool sparse) {
-  return !sparse && rows >= kTileFrom ? kTileRows : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+int64_t item_rows(int64_t rows, int64_t head_dim, bool sparse) {
+  if (!sparse && rows >= kTileFrom) return kTileRows;
+  return rows <= 8 ? 8 : rows <= 16 || head_dim == 128 ? 16 : 32;
 }
 
 struct Workspace {
@@ -55,7 +56,7 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
       num_tokens >= (1ll << 31) ||
       !workspace_args_ok(items, max_q, num_heads, cache->kv_heads, cache->head_dim))
     return FP4IDX_ERR_SHAPE;
-  const int64_t R = item_rows(max_q * (num_heads / cache->kv_heads), sparse);
+  const int64_t R = item_rows(max_q * (num_heads / cache->kv_heads), cache->head_dim, sparse);
   const Workspace w = workspace_of(R, cache->head_dim);
   if (workspace_bytes < (size_t)w.total) return FP4IDX_ERR_SCRATCH;
   if (!dtype_ok(dtype) || !isfinite(softmax_scale)) return FP4IDX_ERR_ARG;
@@ -99,7 +100,7 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
 fp4idx_status launch(AttnArgs& a, int head_dim, bool sparse, int64_t max_tiles, void* stream) {
   const int64_t items = (int64_t)a.batch * a.Hkv * a.rc_max;
   // items of few tiles are not worth cutting: the join costs more than it saves
-  a.split = max_tiles > 8;
+  a.split = max_tiles > 16;
   const int64_t units = a.split ? items * max_tiles : items;
   const int grid = units < kMaxGrid ? (int)units : kMaxGrid;
   if (a.R == kTileRows)
@@ -117,7 +118,8 @@ extern "C" size_t fp4idx_attention_workspace_bytes(int64_t batch, int64_t max_q,
                                                    int64_t head_dim) {
   if (!workspace_args_ok(batch, max_q, num_heads, kv_heads, head_dim)) return 0;
   // of the two forms, the dense one's items are never smaller
-  return (size_t)workspace_of(item_rows(max_q * (num_heads / kv_heads), false), head_dim).total;
+  return (size_t)workspace_of(item_rows(max_q * (num_heads / kv_heads), head_dim, false), head_dim)
+      .total;
 }
 
 extern "C" fp4idx_status fp4idx_paged_attention_fp8(

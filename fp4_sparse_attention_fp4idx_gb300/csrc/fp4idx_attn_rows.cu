@@ -5,22 +5,29 @@
 //
 // What bounds it.  Every visible key and value byte is read once and used for
 // the R = 8, 16 or 32 query rows of an item, so the bound is the memory's
-// bandwidth.  A warp therefore runs alone: it owns 32-key pieces of the
-// cache, which it copies asynchronously into a ring of its own, and keeps its
-// own running softmax and output sums in registers; warps meet only at the
-// end of an item, so no barrier stands between the copies and the arithmetic.
+// bandwidth; below it lies the latency of a warp's chain (fragments, products,
+// softmax, products).  Eight warps compute, each alone on 32-key pieces of the
+// cache with its own running softmax and output sums in registers; they meet
+// only at the end of an item.  Eight others each fill the ring of one of them
+// with asynchronous copies: the walk over pages or selected entries and the
+// copies' issue took a computing warp 950 to 1,900 cycles a piece, next to
+// 1,450 to 2,500 of arithmetic.
 //
 // Mathematics.  Codes are E4M3, exact in fp16; a query row is scaled by a
 // power of two into fp16's range, exact for bf16 and fp16 elements down to
 // 2^-38 of the row's largest, so the products of the score are exact and their
 // sum is fp32.  With the page's scales ks and vs (powers of two), in units of
-// log2:  s = sum(q k) * ks * scale * log2(e).  The running softmax keeps
-// m = max s and l = sum 2^(s-m); the output sums use another reference,
-// M = max (s + log2 vs), the largest contribution so far:
-//   p = 2^(s + log2 vs - M + 14) in fp16,   O = sum p * code,
-// so that a probability is rounded to 2^-11 of itself unless it is 2^-28 or
-// less of the largest contribution, however far the pages' scales lie apart.
-//   out = O * 2^(M - m - 14) / l,   lse = m + log2 l.
+// log2:  s = sum(q k) * ks * scale * log2(e).  The running softmax has two
+// references: m, of the sum l = sum 2^(s-m), and M, of the output sums,
+//   p = 2^(s + log2 vs - M + 10) in fp16,   O = sum p * code,
+// near the largest s and the largest contribution s + log2 vs.  M follows only
+// when a contribution exceeds it by more than 4, m when a score exceeds it by
+// 60: then p <= 2^14, and most pieces need no exchange between lanes and no
+// rescaling.  p is rounded to 2^-11 of itself, or 2^-35 of the largest
+// contribution, however far the pages' scales lie apart.  l is summed from the
+// same exponentials, moved by the references' difference, as long as that and
+// the spread of a piece's scales are small; else it takes its own.
+//   out = O * 2^(M - m - 10) / l,   lse = m + log2 l.
 //
 // Layout.  The scores are computed transposed, S^T = K Q^T, by
 // mma.m16n8k16 with 16 keys and 8 query rows: the keys fill the M side
@@ -41,20 +48,30 @@
 namespace fp4idx_impl {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 8;  // that compute; as many copy
+constexpr int kThreads = 2 * kWarps * 32;
+// Registers of a thread that computes; one that copies has 256 less those (the
+// launch's 128 each, moved).  The least that spill nothing, or next to it: what
+// is spilled goes past the little L1 that the rings leave.
+__host__ __device__ constexpr int compute_regs(int D, int NT, bool sparse) {
+  if (D == 64) return NT == 4 ? 200 : 152;
+  return NT == 1 ? 152 : sparse ? 184 : 192;
+}
 constexpr int kPage = FP4IDX_KV_BLOCK;
 constexpr int kSub = 32;  // keys of a piece: half a page
-constexpr float kShift = 14.0f;
+constexpr float kShift = 10.0f, kSlack = 4.0f, kFar = 60.0f, kSpread = 40.0f;
 
 __host__ __device__ constexpr int stages(int D) { return D == 128 ? 3 : 6; }
 // keys, values, 2 x 32 scales, the mask of visible keys
 __host__ __device__ constexpr int stage_bytes(int D) { return 2 * kSub * D + 256 + 16; }
 __host__ __device__ constexpr int q_row_bytes(int D) { return 2 * D + 32; }
 
+// Where the queries' fragments would not fit the registers.
+__host__ __device__ constexpr bool q_in_smem(int D, int NT) { return D * NT > 128; }
+
 __host__ __device__ constexpr int smem_bytes(int D, int NT) {
   return kWarps * stages(D) * stage_bytes(D) + kWarps * 8 * NT * 3 * 4 +
-         (NT > 2 ? 8 * NT * q_row_bytes(D) : 0);
+         (q_in_smem(D, NT) ? 8 * NT * q_row_bytes(D) : 0) + kWarps * stages(D) * 16;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -67,11 +84,31 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int byt
                : "memory");
 }
 
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Arrives at bar once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Waits for a phase; false when a warp has given up, or after 1 s.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  unsigned long long t0 = 0;
+  for (;;) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    const unsigned long long now = global_ns();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > kWaitLimitNs) {
+      *abort = 1u;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void compute_sync() {  // the warps that compute
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -207,7 +244,7 @@ __device__ __forceinline__ int64_t locate_share(const AttnArgs& a, Cursor<kSpars
     cur.begin = cur.b * per;
     cur.m = seq_of<true>(a, cur.b);
   } else {
-    __shared__ int64_t part[kWarps];
+    __shared__ int64_t part[kThreads / 32];
     __shared__ int64_t found_begin;
     __shared__ int found_b;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -226,7 +263,7 @@ __device__ __forceinline__ int64_t locate_share(const AttnArgs& a, Cursor<kSpars
     if (lane == 31) part[warp] = incl;
     __syncthreads();
     int64_t base = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) base += part[w];
       total += part[w];
     }
@@ -262,7 +299,7 @@ __device__ __forceinline__ int cta_of(int64_t x, int64_t total) {
   return (int)(((x + 1) * grid - 1) / total);
 }
 
-// One warp's copies: a cursor of its own, ahead of the arithmetic.  Dense: a
+// The copies into one ring: a cursor ahead of the arithmetic.  Dense: a
 // piece's page is looked up one piece before its copies.  Sparse: its entries
 // two pieces before, their pages one.
 template <int D, bool kSparse>
@@ -348,9 +385,10 @@ struct Producer {
   }
   // Copies the next piece into the stage at `st` and moves on.  Rows of keys
   // that no query of the item sees are zero-filled.
-  __device__ __forceinline__ void issue(const AttnArgs& a, int64_t s1, uint32_t st, int lane) {
+  __device__ __forceinline__ void issue(const AttnArgs& a, int64_t s1, uint32_t st, uint32_t full,
+                                        int lane) {
     constexpr int kChunks = D / 16;
-    if (have) {
+    {
       const bool page_ok = page >= 0 && page < a.num_blocks;
       bool vis = ok;
       int64_t row_off = 0, sc_off = 0;  // this lane's (sparse) or the piece's (dense) codes
@@ -385,11 +423,13 @@ struct Producer {
         cp_async4(sc + lane * 4, a.ks + sc_off, bytes);
         cp_async4(sc + 128 + lane * 4, a.vs + sc_off, bytes);
       }
-      if (lane == 0)
+      if (lane == 0) {
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc + 256), "r"(mask) : "memory");
+        mbar_arrive(full);
+      }
+      cp_arrive(full);
       locate(a, s1, lane);
     }
-    cp_commit();
   }
 };
 
@@ -410,31 +450,63 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
   constexpr int kStage = stage_bytes(D);
   constexpr int R = 8 * NT;
   constexpr int kChunks = D / 16;  // 16-byte chunks of a row of codes
-  constexpr bool kQSmem = NT > 2;  // the queries' fragments do not fit the registers
+  constexpr bool kQSmem = q_in_smem(D, NT);
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint32_t abort_flag;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int g = lane / 4, t = lane % 4;
-  const uint32_t ring = smem_addr(smem) + warp * S * kStage;
+  const int w8 = warp % kWarps;  // the ring
+  const uint32_t ring = smem_addr(smem) + w8 * S * kStage;
   float* const st_m = reinterpret_cast<float*>(smem + kWarps * S * kStage);  // [warp][row]
   float* const st_M = st_m + kWarps * R;
   float* const st_l = st_M + kWarps * R;
   const uint32_t qs = smem_addr(st_l + kWarps * R);
+  const uint32_t bars = qs + (kQSmem ? R * q_row_bytes(D) : 0);
+  const auto full = [&](int i) { return bars + (w8 * S + i) * 16; };  // stage i is filled
+  const auto empty = [&](int i) { return full(i) + 8; };              // and read
+  volatile uint32_t* const abort = &abort_flag;
 
+  if (tid < kWarps * S) {  // 32 lanes' copies and the mask; the computing warp
+    mbar_init(bars + tid * 16, 33);
+    mbar_init(bars + tid * 16 + 8, 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) abort_flag = 0;
   int64_t s0, s1;
   Cursor<kSparse> cur;
   const int64_t total = locate_share<kSparse>(a, cur, s0, s1);
-  int4 cut = make_int4(0, 0, 0, 0);
   if (s0 >= s1) {
-    if (a.split && tid == 0) a.cuts[blockIdx.x] = cut;
+    if (a.split && tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
+  __syncthreads();
 
-  Producer<D, kSparse> prod;
-  prod.start(a, cur, s0, s1, warp, lane);
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) prod.issue(a, s1, ring + i * kStage, lane);
+  if (warp >= kWarps) {
+    // ---------------------------------------------------------------- copies
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(
+        256 - compute_regs(D, NT, kSparse)));
+    Producer<D, kSparse> prod;
+    prod.start(a, cur, s0, s1, w8, lane);
+    int slot = 0;
+    uint32_t parity = 1;  // of the stage's last release
+    for (int i = 0; prod.have; ++i) {
+      if (i >= S && !__all_sync(kFull, wait_bar(empty(slot), parity, abort))) break;
+      prod.issue(a, s1, ring + slot * kStage, full(slot), lane);
+      if (++slot == S) {
+        slot = 0;
+        parity ^= 1;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(
+      compute_regs(D, NT, kSparse)));
 
-  int slot = 0;  // of the warp's next piece
+  int4 cut = make_int4(0, 0, 0, 0);
+  int slot = 0;         // of the warp's next piece
+  uint32_t parity = 0;  // of its fill
+  bool held = false;    // the slot before it is not released yet
   int xb = 0, x = warp;
   for (int64_t at = s0; at < s1;) {
     const int u = units_of(a, cur.m);
@@ -494,7 +566,7 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
         last[i][1] = cur.m.first + (row0 + 8 * i + 2 * t + 1) / a.G;
       }
     }
-    if constexpr (kQSmem) __syncthreads();
+    if constexpr (kQSmem) compute_sync();
     // a piece within [full_lo, full_hi) or the first tokens is seen by every row
     const int full_hi = cur.m.first + row0 / a.G + 1;
     const int full_lo =
@@ -517,13 +589,17 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
         for (int j = 0; j < 4; ++j) acc[c][i][j] = 0.0f;
 
     for (; x < xe; x += kWarps) {
-      cp_wait<S - 2>();
       __syncwarp();
-      // the slot before this one: every lane is done with it
-      prod.issue(a, s1, ring + (slot == 0 ? S - 1 : slot - 1) * kStage, lane);
+      if (held && lane == 0) mbar_arrive(empty(slot == 0 ? S - 1 : slot - 1));
+      held = true;
+      const bool landed = __all_sync(kFull, wait_bar(full(slot), parity, abort));
       const uint32_t st = ring + slot * kStage;
       const uint32_t sc = st + 2 * kSub * D;
-      slot = slot + 1 == S ? 0 : slot + 1;
+      if (++slot == S) {
+        slot = 0;
+        parity ^= 1;
+      }
+      if (!landed) continue;
       const uint32_t mask = lds32(sc + 256);
       if (mask == 0) continue;
 
@@ -622,44 +698,52 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
           }
       }
       // ---- running softmax
-      uint32_t pb[2][NT][2];
+      // contributions: the scores with their values' scale.  e0: of the piece
+      // (dense), of its first visible key (sparse); kf = 2^(e0 - ev) of a key
+      float e0 = ev[0][0], kf[2][2];
+      bool spread = false;
+      if constexpr (kSparse) {
+        e0 = log2_scale(lds32(sc + 128 + 4 * (__ffs((int)mask) - 1)));
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        float al[2];
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float d = e0 - ev[k][e];
+            spread = spread || ((mask >> (16 * k + 8 * e + g) & 1u) && fabsf(d) > kSpread);
+            kf[k][e] = __int_as_float((127 + (int)fminf(fmaxf(d, -kSpread), kSpread)) << 23);
+          }
+      }
+      bool move = false;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float top = max_g(fmaxf(fmaxf(s[0][i][j], s[0][i][2 + j]),
-                                        fmaxf(s[1][i][j], s[1][i][2 + j])));
-          float topv;
-          if constexpr (kSparse)
-            topv = max_g(fmaxf(fmaxf(s[0][i][j] + ev[0][0], s[0][i][2 + j] + ev[0][1]),
-                               fmaxf(s[1][i][j] + ev[1][0], s[1][i][2 + j] + ev[1][1])));
-          else
-            topv = top + ev[0][0];
-          const float m1 = fmaxf(m[i][j], top), M1 = fmaxf(M[i][j], topv);
-          const float mz = or_zero(m1), Mz = or_zero(M1);
-          l[i][j] *= exp2_approx(m[i][j] - mz);
-          al[j] = exp2_approx(M[i][j] - Mz);
-          m[i][j] = m1;
-          M[i][j] = M1;
-          float sum = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float v = s[k][i][2 * e + j];
-              sum += exp2_approx(v - mz);
-              s[k][i][2 * e + j] =
-                  exp2_approx(v + ((kSparse ? ev[k][e] : ev[0][0]) - Mz + kShift));
-            }
-          l[i][j] += sum;
+          const float a0 = s[0][i][j], a1 = s[0][i][2 + j], a2 = s[1][i][j], a3 = s[1][i][2 + j];
+          const float top = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
+          const float topv = kSparse ? fmaxf(fmaxf(a0 + ev[0][0], a1 + ev[0][1]),
+                                             fmaxf(a2 + ev[1][0], a3 + ev[1][1]))
+                                     : top + e0;
+          move = move || topv > M[i][j] + kSlack || top > m[i][j] + kFar;
         }
+      if (__any_sync(kFull, move)) {  // the references follow the maxima
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          pb[k][i][0] = transpose8(pack16<true>(s[k][i][0], s[k][i][1]));
-          pb[k][i][1] = transpose8(pack16<true>(s[k][i][2], s[k][i][3]));
-        }
-        if (__any_sync(kFull, al[0] != 1.0f || al[1] != 1.0f)) {
+        for (int i = 0; i < NT; ++i) {
+          float al[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float a0 = s[0][i][j], a1 = s[0][i][2 + j], a2 = s[1][i][j],
+                        a3 = s[1][i][2 + j];
+            const float top = max_g(fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)));
+            float topv = top + e0;
+            if constexpr (kSparse)
+              topv = max_g(fmaxf(fmaxf(a0 + ev[0][0], a1 + ev[0][1]),
+                                 fmaxf(a2 + ev[1][0], a3 + ev[1][1])));
+            const float m1 = fmaxf(m[i][j], top), M1 = fmaxf(M[i][j], topv);
+            l[i][j] *= exp2_approx(m[i][j] - or_zero(m1));
+            al[j] = exp2_approx(M[i][j] - or_zero(M1));
+            m[i][j] = m1;
+            M[i][j] = M1;
+          }
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
             acc[c][i][0] *= al[0];
@@ -667,6 +751,43 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
             acc[c][i][2] *= al[0];
             acc[c][i][3] *= al[1];
           }
+        }
+      }
+      // far: the piece's contributions lie so far below M that l loses them
+      bool far = spread;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) far = far || or_zero(M[i][j]) - e0 - or_zero(m[i][j]) > kFar;
+      const bool any_far = __any_sync(kFull, far);
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float mz = or_zero(m[i][j]), Mz = or_zero(M[i][j]);
+          float sum = 0.0f;
+          if (any_far) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) sum += exp2_approx(s[k][i][2 * e + j] - mz);
+          }
+          float w = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& v = s[k][i][2 * e + j];
+              v = exp2_approx(v + ((kSparse ? ev[k][e] : e0) - Mz + kShift));
+              w = kSparse ? fmaf(v, kf[k][e], w) : w + v;
+            }
+          l[i][j] += any_far ? sum : w * exp2_approx(Mz - e0 - kShift - mz);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          pb[k][i][0] = transpose8(pack16<true>(s[k][i][0], s[k][i][1]));
+          pb[k][i][1] = transpose8(pack16<true>(s[k][i][2], s[k][i][3]));
         }
       }
       // ---- output sums: rows g and g + 8 of the fragment are d = 16c + 2g, + 1
@@ -686,10 +807,13 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
       }
     }
 
-    // ---- the warps' sums joined, through each warp's free slot
-    __syncwarp();
-    float* const own =
-        reinterpret_cast<float*>(smem + (warp * S + (slot == 0 ? S - 1 : slot - 1)) * kStage);
+    // ---- the warps' sums joined, through each warp's slot that is not
+    // released yet (a warp without one has no sums)
+    const int free_slot = slot == 0 ? S - 1 : slot - 1;
+    __shared__ int free_of[kWarps];
+    __shared__ float join_f[kWarps][R];  // factor of a warp's sums
+    __shared__ float join_s[2][R];       // of the row: the common factor; lse, log2
+    if (lane == 0) free_of[warp] = free_slot;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -703,53 +827,68 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
       }
     const bool whole = at == cur.begin && end == cur.begin + u;
     const int part = blockIdx.x * 2 + (at == cur.begin && at != s0 ? 1 : 0);
-    __shared__ int free_slot[kWarps];
-    if (lane == 0) free_slot[warp] = slot == 0 ? S - 1 : slot - 1;
-    // a slot holds 16 rows
+    // a slot holds 16 rows; the columns of rows 2t, 2t + 1 are turned by 16 t
+    // floats, so that the lanes of a store lie on different banks
 #pragma unroll
     for (int i0 = 0; i0 < NT; i0 += 2) {
       constexpr int kPer = NT < 2 ? NT : 2;
+      float* const own = reinterpret_cast<float*>(smem + (warp * S + free_slot) * kStage);
+      if (held) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+        for (int i = 0; i < kPer; ++i)
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
+          for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<float2*>(own + (8 * i + 2 * t + j) * D + 16 * c + 2 * g) =
-                make_float2(acc[c][i0 + i][j], acc[c][i0 + i][2 + j]);
-      __syncthreads();
-      for (int e = tid; e < 8 * kPer * D / 4; e += kThreads) {
+            for (int j = 0; j < 2; ++j)
+              *reinterpret_cast<float2*>(own + (8 * i + 2 * t + j) * D + ((16 * c) ^ (16 * t)) +
+                                         2 * g) = make_float2(acc[c][i0 + i][j],
+                                                              acc[c][i0 + i][2 + j]);
+      }
+      compute_sync();
+      if (i0 == 0) {
+        // lane (row, warp): the factors, once for all columns
+        for (int e = tid; e < R * kWarps; e += kWarps * 32) {
+          const int r = e / kWarps, w = e % kWarps;
+          const float mw = st_m[w * R + r], Mw = st_M[w * R + r];
+          float mg = mw, Mg = Mw;
+#pragma unroll
+          for (int d = 1; d < kWarps; d *= 2) {
+            mg = fmaxf(mg, __shfl_xor_sync(kFull, mg, d));
+            Mg = fmaxf(Mg, __shfl_xor_sync(kFull, Mg, d));
+          }
+          float L = mw == -INFINITY ? 0.0f : st_l[w * R + r] * exp2_approx(mw - mg);
+#pragma unroll
+          for (int d = 1; d < kWarps; d *= 2) L += __shfl_xor_sync(kFull, L, d);
+          join_f[w][r] = mw == -INFINITY ? 0.0f : exp2_approx(Mw - Mg);
+          if (w == 0) {
+            join_s[0][r] = mg == -INFINITY ? 0.0f : __frcp_rn(L) * exp2_approx(Mg - mg - kShift);
+            join_s[1][r] = mg == -INFINITY ? -INFINITY : mg + __log2f(L);
+          }
+        }
+        compute_sync();
+      }
+      for (int e = tid; e < 8 * kPer * D / 4; e += kWarps * 32) {
         const int rl = e / (D / 4), d = e % (D / 4) * 4;
         const int r = 8 * i0 + rl;
         if (r >= rows) continue;
-        float mg = -INFINITY, Mg = -INFINITY;
+        const int at_d = rl * D + (d ^ (rl / 2 % 4 * 16));
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          mg = fmaxf(mg, st_m[w * R + r]);
-          Mg = fmaxf(Mg, st_M[w * R + r]);
+          const float f = join_f[w][r];
+          if (f == 0.0f) continue;  // no sums there, or none that count
+          const float4 v = *reinterpret_cast<const float4*>(
+              smem + (w * S + free_of[w]) * kStage + at_d * 4);
+          o.x = fmaf(v.x, f, o.x);
+          o.y = fmaf(v.y, f, o.y);
+          o.z = fmaf(v.z, f, o.z);
+          o.w = fmaf(v.w, f, o.w);
         }
-        float L = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (mg != -INFINITY) {
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            if (st_m[w * R + r] == -INFINITY) continue;
-            L += st_l[w * R + r] * exp2_approx(st_m[w * R + r] - mg);
-            const float f = exp2_approx(st_M[w * R + r] - Mg);
-            const float4 v = *reinterpret_cast<const float4*>(
-                smem + (w * S + free_slot[w]) * kStage + (rl * D + d) * 4);
-            o.x = fmaf(v.x, f, o.x);
-            o.y = fmaf(v.y, f, o.y);
-            o.z = fmaf(v.z, f, o.z);
-            o.w = fmaf(v.w, f, o.w);
-          }
-          const float f = exp2_approx(Mg - mg - kShift), inv = __frcp_rn(L);
-          o.x = o.x * inv * f;
-          o.y = o.y * inv * f;
-          o.z = o.z * inv * f;
-          o.w = o.w * inv * f;
-        }
-        const float lse2 = mg == -INFINITY ? -INFINITY : mg + __log2f(L);
+        const float f = join_s[0][r], lse2 = join_s[1][r];
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
         if (whole) {
           const int tok = cur.m.q0 + (row0 + r) / a.G;
           const int h = head * a.G + (row0 + r) % a.G;
@@ -764,7 +903,7 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
           if (d == 0) a.part_lse[part * R + r] = lse2;
         }
       }
-      __syncthreads();
+      compute_sync();
     }
     if (!whole && at == cur.begin)  // the first fragment of a cut item
       cut = make_int4(cur.b, cur.it - head * cur.m.rcs, head,
@@ -773,8 +912,10 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
     at = end;
     if (at < s1) cur.next(a);
   }
-  if (a.split && tid == 0) a.cuts[blockIdx.x] = cut;
-  cp_wait<0>();
+  if (tid == 0) {
+    if (a.split) a.cuts[blockIdx.x] = cut;
+    if (*abort) flag_error(a.err, FP4IDX_ERRFLAG_TIMEOUT);
+  }
 }
 
 // Joins the partial outputs of the items that a share's end cut: weights
@@ -845,8 +986,9 @@ fp4idx_status launch_one(const AttnArgs& a, int grid, cudaStream_t stream) {
 template <int D, bool kSparse>
 fp4idx_status launch_nt(const AttnArgs& a, int grid, cudaStream_t stream) {
   if (a.R == 8) return launch_one<D, 1, kSparse>(a, grid, stream);
-  if (a.R == 16) return launch_one<D, 2, kSparse>(a, grid, stream);
-  return launch_one<D, 4, kSparse>(a, grid, stream);
+  // 32 rows of 128 columns do not fit the registers
+  if (D == 128 || a.R == 16) return launch_one<D, 2, kSparse>(a, grid, stream);
+  return launch_one<D, D == 64 ? 4 : 2, kSparse>(a, grid, stream);
 }
 
 }  // namespace

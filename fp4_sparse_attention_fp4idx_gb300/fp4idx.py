@@ -722,11 +722,13 @@ class KvCache(ctypes.Structure):
 
 def _fits(t, dtype, ndim, dev, name):
     """t is a CUDA tensor of that type and rank on device `dev`."""
-    torch = _torch()
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda and t.dim() == ndim):
-        _need(t, dtype, name, ndim)  # says what is wrong
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and dev >= 0:
+            return
+    except AttributeError:
+        pass
+    _need(t, dtype, name, ndim)  # says what is wrong
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
 
 
 def _dense(t, shape, name):
@@ -738,9 +740,9 @@ def _type16(t, name):
     """The fp4idx_dtype code of a tensor of bf16 or fp16."""
     torch = _torch()
     dt = getattr(t, "dtype", None)
-    if dt == torch.bfloat16:
+    if dt is torch.bfloat16:
         return DTYPE_BF16
-    if dt == torch.float16:
+    if dt is torch.float16:
         return DTYPE_FP16
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -758,6 +760,27 @@ def _block_strides(t, n, inner, name):
 
 def _kv_cache(k_cache, v_cache, k_scale, v_scale):
     """(KvCache block, device index) of the four tensors."""
+    torch = _torch()
+    codes = (torch.uint8, torch.float8_e4m3fn)
+    try:  # the usual layouts in one test; what fails it is looked at piece by piece
+        shape, st, ss, dev = k_cache.shape, k_cache.stride(), k_scale.stride(), \
+            k_cache.get_device()
+        B, H, n, D = shape
+        if (k_cache.dtype in codes and v_cache.dtype in codes and
+                k_scale.dtype is torch.float32 and v_scale.dtype is torch.float32 and
+                n == KV_BLOCK and (D == 128 or D == 64) and B > 1 and H > 1 and dev >= 0 and
+                v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == dev and
+                v_cache.shape == shape and k_scale.shape == v_scale.shape == (B, H) and
+                v_cache.stride() == st and v_scale.stride() == ss and ss[1] == 1 and
+                st[1:] == (KV_BLOCK * D, D, 1)):
+            return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                           v_scale.data_ptr(), B, st[0], ss[0], H, D), dev
+    except (AttributeError, ValueError):
+        pass
+    return _kv_cache_slow(k_cache, v_cache, k_scale, v_scale)
+
+
+def _kv_cache_slow(k_cache, v_cache, k_scale, v_scale):
     torch = _torch()
     f8, f32 = torch.float8_e4m3fn, torch.float32
     dev = k_cache.get_device() if isinstance(k_cache, torch.Tensor) else -1
@@ -892,18 +915,19 @@ def _attention_buffers(q, c, dev, block_table, out, lse, workspace, batch, max_q
     if block_table.shape[1] > 1 and block_table.stride(1) != 1:
         raise ValueError("block_table must have unit column stride")
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, H, D))
     else:
         _fits(out, q.dtype, 3, dev, "out")
         _dense(out, (T, H, D), "out")
+    device = out.device
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = torch.empty((T, H), dtype=torch.float32, device=device)
     else:
         _fits(lse, torch.float32, 2, dev, "lse")
         _dense(lse, (T, H), "lse")
     if workspace is None:
         need = _lib.fp4idx_attention_workspace_bytes(batch, max_q, H, c.kv_heads, D)
-        workspace = torch.empty(need or 16, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(need or 16, dtype=torch.uint8, device=device)
     else:
         _fits(workspace, torch.uint8, 1, dev, "workspace")
         _dense(workspace, workspace.shape, "workspace")
