@@ -9,15 +9,31 @@ namespace {
 
 constexpr int kPage = FP4IDX_KV_BLOCK;
 
-// From this many query rows per sequence and key head on, the tensor-core
-// kernel of 256-row items (fp4idx_attn_tiles.cu) takes the call.
-constexpr int64_t kTileFrom = 128;
+// The tensor-core kernel of 256-row items (fp4idx_attn_tiles.cu) takes dense
+// calls of at least kTileFrom query rows per sequence and key head and of more
+// than kTileWork query rows x 64-key tiles in all.  Measured, the kernel for few
+// rows against it, us: 64 sequences x 8 key heads of 8192 keys, 32 rows 338 /
+// 323, 64 rows 660 / 328; of 500 keys and 500 tokens x 4 rows, 4 sequences x 2
+// key heads (900 row-tiles a CTA) 28 / 40, x 8 key heads (3700) 93 / 39.
+constexpr int64_t kTileFrom = 33;
+constexpr int64_t kTileWork = 1200 * kMaxGrid;
 constexpr int64_t kTileRows = 256;
 
-// Query rows of an item; selected tokens never take the tensor-core kernel.
-int64_t item_rows(int64_t rows, int64_t head_dim, bool sparse) {
-  if (!sparse && rows >= kTileFrom) return kTileRows;
+// Query rows of an item of the kernel for few rows (fp4idx_attn_rows.cu).
+int64_t item_rows(int64_t rows, int64_t head_dim) {
   return rows <= 8 ? 8 : rows <= 16 || head_dim == 128 ? 16 : 32;
+}
+
+// Whether items are cut where the CTAs' equal shares end, and joined, or each
+// is one CTA's.  Cutting saves what the fullest CTA has more than the mean, up to
+// one item's tiles, and costs another item's start and end per CTA, the more
+// the more rows, and the join.  Measured, cut against whole, us: 8 items of 32
+// tiles 10.7 / 16.4, 240 of 32 tiles 37 / 30, 160 of 63 tiles 40 / 43; of 32
+// rows, 80 items of 32 tiles 62 / 39.  Selected tokens cost twice as much a tile.
+bool worth_cutting(int64_t items, int64_t tiles, int64_t rows, bool sparse) {
+  const int64_t rounds = (items + kMaxGrid - 1) / kMaxGrid;
+  const int64_t saved = (rounds * kMaxGrid - items) * tiles;  // tiles x CTAs
+  return saved * (sparse ? 2 : 1) > (16 + rows) * rounds * kMaxGrid;
 }
 
 struct Workspace {
@@ -49,14 +65,17 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
                           const int32_t* block_table, int64_t block_table_stride,
                           float softmax_scale, void* out, float* lse, int64_t items,
                           int64_t max_q, int64_t num_tokens, int64_t num_heads, void* workspace,
-                          size_t workspace_bytes, uint32_t* err_flags, bool sparse) {
+                          size_t workspace_bytes, uint32_t* err_flags, bool sparse,
+                          int64_t tiles) {
   const fp4idx_status cs = check_cache(cache);
   if (cs == FP4IDX_ERR_NULL || !q || !block_table || !out || !workspace) return FP4IDX_ERR_NULL;
   if (cs == FP4IDX_ERR_SHAPE || num_heads < 1 || num_heads % cache->kv_heads ||
       num_tokens >= (1ll << 31) ||
       !workspace_args_ok(items, max_q, num_heads, cache->kv_heads, cache->head_dim))
     return FP4IDX_ERR_SHAPE;
-  const int64_t R = item_rows(max_q * (num_heads / cache->kv_heads), cache->head_dim, sparse);
+  const int64_t rows = max_q * (num_heads / cache->kv_heads);
+  const bool few = sparse || rows < kTileFrom || items * cache->kv_heads * rows * tiles <= kTileWork;
+  const int64_t R = few ? item_rows(rows, cache->head_dim) : kTileRows;
   const Workspace w = workspace_of(R, cache->head_dim);
   if (workspace_bytes < (size_t)w.total) return FP4IDX_ERR_SCRATCH;
   if (!dtype_ok(dtype) || !isfinite(softmax_scale)) return FP4IDX_ERR_ARG;
@@ -99,8 +118,8 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
 // `max_tiles`: 64-key tiles of an item, at most.
 fp4idx_status launch(AttnArgs& a, int head_dim, bool sparse, int64_t max_tiles, void* stream) {
   const int64_t items = (int64_t)a.batch * a.Hkv * a.rc_max;
-  // items of few tiles are not worth cutting: the join costs more than it saves
-  a.split = max_tiles > 16;
+  // the tensor-core kernel always cuts
+  a.split = a.R == kTileRows || worth_cutting(items, max_tiles, a.R, sparse);
   const int64_t units = a.split ? items * max_tiles : items;
   const int grid = units < kMaxGrid ? (int)units : kMaxGrid;
   if (a.R == kTileRows)
@@ -117,8 +136,8 @@ extern "C" size_t fp4idx_attention_workspace_bytes(int64_t batch, int64_t max_q,
                                                    int64_t num_heads, int64_t kv_heads,
                                                    int64_t head_dim) {
   if (!workspace_args_ok(batch, max_q, num_heads, kv_heads, head_dim)) return 0;
-  // of the two forms, the dense one's items are never smaller
-  return (size_t)workspace_of(item_rows(max_q * (num_heads / kv_heads), head_dim, false), head_dim)
+  const int64_t rows = max_q * (num_heads / kv_heads);
+  return (size_t)workspace_of(rows < kTileFrom ? item_rows(rows, head_dim) : kTileRows, head_dim)
       .total;
 }
 
@@ -142,15 +161,6 @@ extern "C" fp4idx_status fp4idx_paged_attention_fp8(
     return FP4IDX_ERR_SHAPE;
   if (window < 0 || sinks < 0) return FP4IDX_ERR_ARG;
   AttnArgs a = {};
-  const fp4idx_status st =
-      common_args(a, q, q_token_stride, q_head_stride, dtype, cache, block_table,
-                  block_table_stride, softmax_scale, out, lse, batch, max_q, num_tokens, num_heads,
-                  workspace, workspace_bytes, err_flags, false);
-  if (st != FP4IDX_OK) return st;
-  if (!aligned(context_lens, 4) || !aligned(q_starts, 4)) return FP4IDX_ERR_ALIGN;
-  a.ctx = context_lens;
-  a.starts = q_starts;
-  a.max_context = (int32_t)max_context;
   // a window that holds every context is no window
   a.window = window < max_context ? (int32_t)window : 0;
   a.sinks = (int32_t)(sinks < max_context ? sinks : max_context);
@@ -159,7 +169,17 @@ extern "C" fp4idx_status fp4idx_paged_attention_fp8(
     const int64_t seen = (a.window + max_q + kPage - 1) / kPage + 1 + (a.sinks + kPage - 1) / kPage;
     if (seen < tiles) tiles = seen;
   }
-  return launch(a, cache->head_dim, false, tiles < 1 ? 1 : tiles, stream);
+  if (tiles < 1) tiles = 1;
+  const fp4idx_status st =
+      common_args(a, q, q_token_stride, q_head_stride, dtype, cache, block_table,
+                  block_table_stride, softmax_scale, out, lse, batch, max_q, num_tokens, num_heads,
+                  workspace, workspace_bytes, err_flags, false, tiles);
+  if (st != FP4IDX_OK) return st;
+  if (!aligned(context_lens, 4) || !aligned(q_starts, 4)) return FP4IDX_ERR_ALIGN;
+  a.ctx = context_lens;
+  a.starts = q_starts;
+  a.max_context = (int32_t)max_context;
+  return launch(a, cache->head_dim, false, tiles, stream);
 }
 
 extern "C" fp4idx_status fp4idx_sparse_attention_fp8(
@@ -181,7 +201,7 @@ extern "C" fp4idx_status fp4idx_sparse_attention_fp8(
   const fp4idx_status st = common_args(a, q, q_token_stride, q_head_stride, dtype, cache,
                                        block_table, block_table_stride, softmax_scale, out, lse,
                                        num_tokens, 1, num_tokens, num_heads, workspace,
-                                       workspace_bytes, err_flags, true);
+                                       workspace_bytes, err_flags, true, 1);
   if (st != FP4IDX_OK) return st;
   if (!aligned(seq_ids, 4) || !aligned(indices, 4)) return FP4IDX_ERR_ALIGN;
   a.seq_ids = seq_ids;

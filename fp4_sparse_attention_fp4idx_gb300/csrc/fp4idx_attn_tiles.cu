@@ -328,6 +328,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // The largest of 32 values, two to an instruction in four chains.
 __device__ __forceinline__ float top32(const float* s) {
   float x[4] = {s[0], s[1], s[2], s[3]};
@@ -433,6 +440,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
   volatile uint32_t* abort = &ctl.abort;
   const auto bar = [&](int i) { return smem_addr(&ctl.bars[i]); };
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // joins as CTAs end
   locate_share(a, ctl.share);
   const Share& share = ctl.share;
   if (share.s0 >= share.s1) {
@@ -486,43 +494,54 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
       const bool live_row = r < m.row0 + m.rows;
       const int tok = m.q0 + r / a.G, h = seg.head * a.G + r % a.G;
       const bool live = live_row && tok >= 0 && tok < a.T;
-      // ---- this row of Q, scaled by a power of two, into shared memory
+      // ---- the warp's rows of Q into shared memory, kRowLanes lanes to a row,
+      // and scaled there by powers of two.  (Loops that stay loops: what runs
+      // once per item is cold code, and its fetch costs more than its steps.)
       float fac;
       {
-        const uint16_t* src = a.q + (live ? tok * a.q_ts + h * a.q_hs : 0);
-        float amax = 0.0f;
+        constexpr int kRowLanes = D / 8, kPer = 32 / kRowLanes;
+        const int64_t own = live ? tok * a.q_ts + h * a.q_hs : -1;  // of the lane's row
+        const int c = lane % kRowLanes, row = warp % 4 * 32 + lane / kRowLanes;
+        const uint32_t dst = sq + half * kHalves * kQHalf + c / 8 * kQHalf + row * 128;
+#pragma unroll 1
+        for (int i = 0; i < kRowLanes; ++i) {
+          const int64_t off = __shfl_sync(kFull, own, i * kPer + lane / kRowLanes);
+          const uint32_t at = dst + i * kPer * 128 + ((c ^ (row + i * kPer)) & 7) * 16;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at),
+                       "l"(a.q + (off < 0 ? 0 : off + c * 8)), "r"(off < 0 ? 0 : 16)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        // the lane's own row; magnitudes compare as their bits do
+        const uint32_t src = sq + half * kHalves * kQHalf + rl * 128;
+        const auto chunk = [&](int k) {
+          return src + k / 8 * kQHalf + ((k ^ rl) & 7) * 16;
+        };
+        uint32_t top = 0;
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (live) w = __ldg(reinterpret_cast<const uint4*>(src) + c);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int k = 0; k < kRowLanes; ++k) {
+          uint32_t u[4];
+          lds128(chunk(k), u);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack16(a.half, u[j]);
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
+          for (int j = 0; j < 4; ++j) top = __vmaxu2(top, u[j] & 0x7fff7fffu);
         }
-        const uint32_t b = max(__float_as_uint(amax) >> 23, 15u);
-        float up = __uint_as_float((268u - b) << 23);
-        fac = a.scale_log2 * __uint_as_float((b - 14u) << 23);
-        if (fac < 0.0f) {
-          fac = -fac;
-          up = -up;
-        }
-        const uint32_t dst = sq + half * kHalves * kQHalf + rl * 128;
+        const float2 both = unpack16(a.half, top);
+        // the largest * 2^(141 - b) lies in [2^14, 2^15) for its biased exponent b
+        const uint32_t b = max(__float_as_uint(fmaxf(both.x, both.y)) >> 23, 15u);
+        const float up = __uint_as_float((268u - b) << 23 | (uint32_t)(a.scale_log2 < 0.0f) << 31);
+        fac = fabsf(a.scale_log2) * __uint_as_float((b - 14u) << 23);
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (live) w = __ldg(reinterpret_cast<const uint4*>(src) + c);
-          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int k = 0; k < kRowLanes; ++k) {
+          uint32_t u[4];
+          lds128(chunk(k), u);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 f = unpack16(a.half, u[j]);
             u[j] = pack16<true>(f.x * up, f.y * up);
           }
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                           dst + c / 8 * kQHalf + ((c % 8) ^ (rl & 7)) * 16),
-                       "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(chunk(k)), "r"(u[0]),
+                       "r"(u[1]), "r"(u[2]), "r"(u[3])
                        : "memory");
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -558,7 +577,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
             tmem_ld32(ts + page * kPage, s);
             tmem_ld32(ts + page * kPage + 32, s + 32);
             tmem_wait_ld();
-            if (!full) {
+            if (__builtin_expect(!full, 0)) {
 #pragma unroll
               for (int w = 0; w < 2; ++w) {
                 const int from = kb + page * kPage + w * 32;
@@ -578,7 +597,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
           const float M1 = fmaxf(x0 + e0, x1 + e1);
           // ---- O's reference, moved seldom
           const bool move = M1 > MM + kSlack || (MM == -INFINITY && M1 != -INFINITY);
-          if (__any_sync(kFull, move)) {
+          if (__builtin_expect(__any_sync(kFull, move), 0)) {
             const float al = move ? exp2_approx(MM - M1) : 1.0f;
             if (move) MM = M1;
             if (t > 0) {
@@ -611,7 +630,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const float* v = s + w * 32;
-              if (any_far) {
+              if (__builtin_expect(any_far, 0)) {
 #pragma unroll
                 for (int q = 0; q < 32; ++q) own += exp2_approx(fmaf(v[q], c, -mz));
               }
@@ -1003,36 +1022,47 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(const AttnArgs a) {
   item_of(a, cut.x, cut.y, m);
   const int lane = threadIdx.x % 32;
   const auto slot = [&](int f) { return (int64_t)2 * (cta + f) + (f == 0 ? cut.w & 1 : 0); };
-  constexpr int kV = D / 32;
-  for (int k = 0; k < 4; ++k) {
-    const int rl = blockIdx.x % kBlocks * 32 + threadIdx.x / 32 * 4 + k;
-    const int r = m.row0 + rl;
-    const int tok = m.q0 + r / a.G;
-    if (rl >= m.rows || tok < 0 || tok >= a.T) continue;
-    float top = -INFINITY;
-    for (int f = 0; f < n; ++f) top = fmaxf(top, a.part_lse[slot(f) * kItemRows + rl]);
-    float o[kV], den = 0.0f;
+  constexpr int kV = D / 32, kRows = 4;
+  const int r0 = blockIdx.x % kBlocks * 32 + threadIdx.x / 32 * kRows;
+  if (r0 >= m.rows) return;
+  float top[kRows], den[kRows], o[kRows][kV];
 #pragma unroll
-    for (int j = 0; j < kV; ++j) o[j] = 0.0f;
-    if (top != -INFINITY) {
-#pragma unroll 4
-      for (int f = 0; f < n; ++f) {
-        const int64_t row = slot(f) * kItemRows + rl;
-        const float w = exp2_approx(a.part_lse[row] - top);
-        den += w;
+  for (int k = 0; k < kRows; ++k) {
+    top[k] = -INFINITY;
+    den[k] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) o[j] = fmaf(a.part_out[row * D + lane * kV + j], w, o[j]);
-      }
-      const float inv = __frcp_rn(den);
+    for (int j = 0; j < kV; ++j) o[k][j] = 0.0f;
+  }
+#pragma unroll 2
+  for (int f = 0; f < n; ++f)
 #pragma unroll
-      for (int j = 0; j < kV; ++j) o[j] *= inv;
+    for (int k = 0; k < kRows; ++k)
+      if (r0 + k < m.rows) top[k] = fmaxf(top[k], a.part_lse[slot(f) * kItemRows + r0 + k]);
+#pragma unroll 2
+  for (int f = 0; f < n; ++f)
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (r0 + k >= m.rows || top[k] == -INFINITY) continue;
+      const int64_t row = slot(f) * kItemRows + r0 + k;
+      const float w = exp2_approx(a.part_lse[row] - top[k]);
+      den[k] += w;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) o[k][j] = fmaf(a.part_out[row * D + lane * kV + j], w, o[k][j]);
     }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int r = m.row0 + r0 + k;
+    const int tok = m.q0 + r / a.G;
+    if (r0 + k >= m.rows || tok < 0 || tok >= a.T) continue;
+    const bool some = top[k] != -INFINITY;
+    const float inv = some ? __frcp_rn(den[k]) : 0.0f;
     const int64_t orow = (int64_t)tok * a.Hq + cut.z * a.G + r % a.G;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * kV);
 #pragma unroll
-    for (int j = 0; j < kV; j += 2) dst[j / 2] = pack16(a.half, o[j], o[j + 1]);
+    for (int j = 0; j < kV; j += 2)
+      dst[j / 2] = pack16(a.half, o[k][j] * inv, o[k][j + 1] * inv);
     if (a.lse && lane == 0)
-      a.lse[orow] = top == -INFINITY ? -INFINITY : (top + __log2f(den)) * kLn2;
+      a.lse[orow] = some ? (top[k] + __log2f(den[k])) * kLn2 : -INFINITY;
   }
 }
 
