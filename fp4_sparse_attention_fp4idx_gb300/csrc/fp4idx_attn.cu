@@ -13,7 +13,7 @@ constexpr int kPage = FP4IDX_KV_BLOCK;
 // calls of at least kTileFrom query rows per sequence and key head and of more
 // than kTileWork query rows x 64-key tiles in all.  Measured, the kernel for few
 // rows against it, us: 64 sequences x 8 key heads of 8192 keys, 32 rows 338 /
-// 323, 64 rows 660 / 328; of 500 keys and 500 tokens x 4 rows, 4 sequences x 2
+// 323, 64 rows 660 / 324; of 500 keys and 500 tokens x 4 rows, 4 sequences x 2
 // key heads (900 row-tiles a CTA) 28 / 40, x 8 key heads (3700) 93 / 39.
 constexpr int64_t kTileFrom = 33;
 constexpr int64_t kTileWork = 1200 * kMaxGrid;
@@ -25,15 +25,18 @@ int64_t item_rows(int64_t rows, int64_t head_dim) {
 }
 
 // Whether items are cut where the CTAs' equal shares end, and joined, or each
-// is one CTA's.  Cutting saves what the fullest CTA has more than the mean, up to
-// one item's tiles, and costs another item's start and end per CTA, the more
-// the more rows, and the join.  Measured, cut against whole, us: 8 items of 32
-// tiles 10.7 / 16.4, 240 of 32 tiles 37 / 30, 160 of 63 tiles 40 / 43; of 32
-// rows, 80 items of 32 tiles 62 / 39.  Selected tokens cost twice as much a tile.
+// is one CTA's.  Cutting saves what the fullest CTA has more than the mean: up
+// to one item's tiles, and where lengths differ perhaps a quarter of the rest.
+// It costs each CTA another item's start and end, the more the more rows, and
+// the join.  Measured, cut against whole, us: 8 items of 32 tiles 10.7 / 16.4,
+// 240 of 32 tiles 37 / 30, of 94 tiles 65 / 70, 160 of 63 tiles 40 / 43; 80 of
+// 32 rows and 32 tiles 62 / 39, 1024 of 16 rows and 128 tiles 338 / 380.
+// Selected tokens cost twice as much a tile, and their items are equal.
 bool worth_cutting(int64_t items, int64_t tiles, int64_t rows, bool sparse) {
   const int64_t rounds = (items + kMaxGrid - 1) / kMaxGrid;
-  const int64_t saved = (rounds * kMaxGrid - items) * tiles;  // tiles x CTAs
-  return saved * (sparse ? 2 : 1) > (16 + rows) * rounds * kMaxGrid;
+  int64_t saved = (rounds * kMaxGrid - items) * tiles;  // tiles x CTAs
+  saved += sparse ? saved : items * tiles / 4;
+  return saved > (14 + rows) * rounds * kMaxGrid;
 }
 
 struct Workspace {

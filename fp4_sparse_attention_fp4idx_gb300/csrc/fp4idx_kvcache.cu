@@ -195,42 +195,49 @@ struct LoadArgs {
   uint32_t* err;
 };
 
-// grid (blocks over (token, head) rows, 1, keys / values): D/16 lanes a row,
-// 16 codes each, written as two 16-byte words.
+// A thread per 16 codes of a (token, head) row, keys and values: D/16 lanes a
+// row, each code read as one 16-byte word and written as two.
 template <int D, bool kHalf>
 __global__ __launch_bounds__(256) void kv_load_kernel(LoadArgs a) {
   constexpr int kLanes = D / 16;
-  const LoadSide side = blockIdx.z ? a.v : a.k;
   const int64_t rows = a.T * a.heads;
   const int c = threadIdx.x % kLanes;
   for (int64_t r = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes; r < rows;
        r += (int64_t)gridDim.x * (256 / kLanes)) {
-    const int64_t t = r / a.heads;
+    const int64_t t = rows < (1ll << 32) ? (uint32_t)r / (uint32_t)a.heads : r / a.heads;
     const int h = (int)(r - t * a.heads);
     const int64_t slot = __ldg(a.slots + t);
     if (slot < 0) continue;
     if (slot >= a.num_blocks * kPage) {
-      if (h == 0 && blockIdx.z == 0 && c == 0) flag_error(a.err, FP4IDX_ERRFLAG_SLOT);
+      if (h == 0 && c == 0) flag_error(a.err, FP4IDX_ERRFLAG_SLOT);
       continue;
     }
     const int64_t page = slot / kPage;
     const int off = (int)(slot % kPage);
-    const uint4 w = *reinterpret_cast<const uint4*>(side.codes + page * a.code_stride +
-                                                    ((int64_t)h * kPage + off) * D + c * 16);
-    const float s = side.scale[page * a.scale_stride + h];
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    uint32_t o[8];
+    const int64_t at = page * a.code_stride + ((int64_t)h * kPage + off) * D + c * 16;
+    const int64_t sc = page * a.scale_stride + h;
+    uint4 w[2];
+    float s[2];
+    w[0] = *reinterpret_cast<const uint4*>(a.k.codes + at);
+    w[1] = *reinterpret_cast<const uint4*>(a.v.codes + at);
+    s[0] = a.k.scale[sc];
+    s[1] = a.v.scale[sc];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t lo, hi;
-      e4m3x4_to_f16x2(u[j], lo, hi);
-      const float2 f = unpack16<true>(lo), g = unpack16<true>(hi);
-      o[2 * j] = pack16<kHalf>(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
-      o[2 * j + 1] = pack16<kHalf>(__fmul_rn(g.x, s), __fmul_rn(g.y, s));
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16x2(u[j], lo, hi);
+        const float2 f = unpack16<true>(lo), g = unpack16<true>(hi);
+        o[2 * j] = pack16<kHalf>(__fmul_rn(f.x, s[e]), __fmul_rn(f.y, s[e]));
+        o[2 * j + 1] = pack16<kHalf>(__fmul_rn(g.x, s[e]), __fmul_rn(g.y, s[e]));
+      }
+      uint4* dst = reinterpret_cast<uint4*>((e ? a.v.out : a.k.out) + r * D + c * 16);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
-    uint4* dst = reinterpret_cast<uint4*>(side.out + r * D + c * 16);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -311,10 +318,10 @@ extern "C" fp4idx_status fp4idx_kv_load_fp8(const fp4idx_kv_cache* cache,
   a.err = err_flags;
   const int rows_per_block = 256 * 16 / cache->head_dim;
   const int64_t want = (num_tokens * a.heads + rows_per_block - 1) / rows_per_block;
-  const dim3 grid((unsigned)(want < (1 << 30) ? want : (1 << 30)), 1, 2);
+  const unsigned grid = (unsigned)(want < (1 << 30) ? want : (1 << 30));
   const bool half = dtype == FP4IDX_FP16;
   auto* kern = cache->head_dim == 128
                    ? (half ? kv_load_kernel<128, true> : kv_load_kernel<128, false>)
                    : (half ? kv_load_kernel<64, true> : kv_load_kernel<64, false>);
-  return launch3(kern, grid, 256, stream, a) == cudaSuccess ? FP4IDX_OK : FP4IDX_ERR_CUDA;
+  return launch3(kern, dim3(grid), 256, stream, a) == cudaSuccess ? FP4IDX_OK : FP4IDX_ERR_CUDA;
 }

@@ -40,7 +40,7 @@ constexpr int kCluster = 8;
 
 // Candidates that fit.  The threshold lets through k + 4 sigma of the sampled
 // rank: about 1.6 k at k = 2048 of 65,536.
-constexpr int cap_of(int k) { return k <= 1024 ? 3072 : k * 9 / 4; }
+constexpr int cap_of(int k) { return k <= 1024 ? 3200 : k * 9 / 4; }
 
 struct TopkArgs {
   const float* logits;
@@ -362,15 +362,6 @@ __global__ __launch_bounds__(kThreads, kClustered ? 1 : 4) void topk_kernel(cons
   int n = a.lens ? a.lens[row] : a.cols;
   n = n < 0 ? 0 : n > a.cols ? a.cols : n;
   if (!kClustered && a.map_words == 0) return select_general(a, x, n, out, row, sh);
-  // the row starts on its way to L2 while its samples are looked at
-  if (rank == 0 && n > a.cap && tid < 32) {
-    constexpr int kPiece = 4096;  // entries
-    const int head = (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) / 4 % 4);
-    for (int at = head + lane * kPiece; at + 4 <= n; at += 32 * kPiece)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x + at),
-                   "r"(min(kPiece, (n - at) / 4 * 4) * 4)
-                   : "memory");
-  }
   const int words = (n + 31) / 32;
   for (int i = tid; i < words; i += kThreads) map[i] = 0;
   if (tid == 0) sh.count = 0;

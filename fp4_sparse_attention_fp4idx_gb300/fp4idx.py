@@ -15,6 +15,7 @@ Two layers:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -901,18 +902,25 @@ def attention_workspace_bytes(batch: int, max_q: int, num_heads: int, kv_heads: 
     return _lib.fp4idx_attention_workspace_bytes(batch, max_q, num_heads, kv_heads, head_dim)
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(batch, max_q, num_heads, kv_heads, head_dim):
+    """At least 16, so that an empty call has an address to pass."""
+    return attention_workspace_bytes(batch, max_q, num_heads, kv_heads, head_dim) or 16
+
+
 def _attention_buffers(q, c, dev, block_table, out, lse, workspace, batch, max_q):
     """Checks of q and block_table; (dtype code, strides of q, out, lse,
     workspace), allocated where not given."""
     torch = _torch()
     dt = _type16(q, "q")
-    D = c.head_dim
-    if q.dim() != 3 or q.shape[1] % c.kv_heads:
+    H_kv, D = c.kv_heads, c.head_dim
+    shape = q.shape
+    if len(shape) != 3 or shape[1] % H_kv:
         raise ValueError("q must be [T, H, D], H a multiple of the cache's heads")
-    T, H = q.shape[0], q.shape[1]
+    T, H, _ = shape
     qt, qh = _rows16(q, H, D, dev, "q")
     _fits(block_table, torch.int32, 2, dev, "block_table")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+    if block_table.stride(1) != 1 and block_table.shape[1] > 1:
         raise ValueError("block_table must have unit column stride")
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, H, D))
@@ -926,8 +934,8 @@ def _attention_buffers(q, c, dev, block_table, out, lse, workspace, batch, max_q
         _fits(lse, torch.float32, 2, dev, "lse")
         _dense(lse, (T, H), "lse")
     if workspace is None:
-        need = _lib.fp4idx_attention_workspace_bytes(batch, max_q, H, c.kv_heads, D)
-        workspace = torch.empty(need or 16, dtype=torch.uint8, device=device)
+        workspace = torch.empty(_workspace_bytes(batch, max_q, H, H_kv, D), dtype=torch.uint8,
+                                device=device)
     else:
         _fits(workspace, torch.uint8, 1, dev, "workspace")
         _dense(workspace, workspace.shape, "workspace")
@@ -949,7 +957,7 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cont
     c, dev = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     _type16(q, "q")
     _fits(context_lens, torch.int32, 1, dev, "context_lens")
-    T, batch = q.shape[0], context_lens.shape[0]
+    T, batch = len(q), len(context_lens)
     _dense(context_lens, (batch,), "context_lens")
     starts = None
     if q_starts is not None:
