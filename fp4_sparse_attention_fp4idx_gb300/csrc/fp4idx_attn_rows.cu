@@ -541,8 +541,8 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
       // amax * 2^(141 - b) lies in [2^14, 2^15) for its biased exponent b
       const uint32_t b = max(__float_as_uint(amax) >> 23, 15u);
-      const float up = __uint_as_float((268u - b) << 23);
-      const float f = a.scale_log2 * __uint_as_float((b - 14u) << 23);
+      const float up = __uint_as_float((268u - b) << 23 | (uint32_t)(a.scale_log2 < 0.0f) << 31);
+      const float f = fabsf(a.scale_log2) * __uint_as_float((b - 14u) << 23);
       fac[i][0] = __shfl_sync(kFull, f, 8 * t);
       fac[i][1] = __shfl_sync(kFull, f, 8 * t + 4);
 #pragma unroll
@@ -667,15 +667,22 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
         key0 = tile * kPage + ((x - xb) & 1) * kSub;
         full = full && key0 + kSub <= full_hi && (key0 >= full_lo || key0 + kSub <= a.sinks);
       }
+      // a piece of one page: the factor is not negative, so the largest sum
+      // gives the largest score, and the products join the exponents' fma.  (A
+      // factor of zero would make a masked score NaN.)
+      float cf[NT][2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int j = 0; j < 2; ++j) {
+          cf[i][j] = kSparse ? 1.0f : fmaxf(ks[0][0] * fac[i][j], 0x1p-100f);
+          if constexpr (kSparse) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float f = (kSparse ? ks[k][j / 2] : ks[0][0]) * fac[i][j % 2];
-            s[k][i][j] *= f;
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) s[k][i][2 * e + j] *= ks[k][e] * fac[i][j];
           }
+        }
       if (!full) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -719,7 +726,7 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float a0 = s[0][i][j], a1 = s[0][i][2 + j], a2 = s[1][i][j], a3 = s[1][i][2 + j];
-          const float top = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
+          const float top = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * cf[i][j];
           const float topv = kSparse ? fmaxf(fmaxf(a0 + ev[0][0], a1 + ev[0][1]),
                                              fmaxf(a2 + ev[1][0], a3 + ev[1][1]))
                                      : top + e0;
@@ -733,7 +740,7 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
           for (int j = 0; j < 2; ++j) {
             const float a0 = s[0][i][j], a1 = s[0][i][2 + j], a2 = s[1][i][j],
                         a3 = s[1][i][2 + j];
-            const float top = max_g(fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)));
+            const float top = max_g(fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * cf[i][j]);
             float topv = top + e0;
             if constexpr (kSparse)
               topv = max_g(fmaxf(fmaxf(a0 + ev[0][0], a1 + ev[0][1]),
@@ -771,7 +778,7 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) sum += exp2_approx(s[k][i][2 * e + j] - mz);
+              for (int e = 0; e < 2; ++e) sum += exp2_approx(fmaf(s[k][i][2 * e + j], cf[i][j], -mz));
           }
           float w = 0.0f;
 #pragma unroll
@@ -779,7 +786,7 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float& v = s[k][i][2 * e + j];
-              v = exp2_approx(v + ((kSparse ? ev[k][e] : e0) - Mz + kShift));
+              v = exp2_approx(fmaf(v, cf[i][j], (kSparse ? ev[k][e] : e0) - Mz + kShift));
               w = kSparse ? fmaf(v, kf[k][e], w) : w + v;
             }
           l[i][j] += any_far ? sum : w * exp2_approx(Mz - e0 - kShift - mz);
