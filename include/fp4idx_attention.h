@@ -121,8 +121,9 @@ fp4idx_status fp4idx_kv_load_fp8(const fp4idx_kv_cache* cache, const int64_t* sl
  * reads key head h / (num_heads / kv_heads).
  *
  * The products of keys and queries are exact in the tensor core, the softmax
- * and both sums are fp32; probabilities are rounded to fp16 relative to the
- * row's largest contribution (2^-11) before the product with the values.
+ * and both sums are fp32; probabilities are rounded to fp16 before the product
+ * with the values, by 2^-11 of themselves or 2^-35 of the row's largest
+ * contribution.
  *
  *   q             16-bit, row (t, h) at t*q_token_stride + h*q_head_stride
  *                 elements; 16-byte aligned, strides multiples of 8.  The
@@ -131,6 +132,8 @@ fp4idx_status fp4idx_kv_load_fp8(const fp4idx_kv_cache* cache, const int64_t* sl
  *                 read for the pages that hold visible keys only;
  *                 block_table_stride >= ceil(max_context / 64).
  *   context_lens  int32 [batch]; values are taken within [0, max_context].
+ *   max_context   a bound on context_lens.  Kernel and work split are chosen
+ *                 by it, so a loose one costs time, not correctness.
  *   q_starts      int32 [batch+1], ascending from 0 to num_tokens, or NULL.
  *   max_q         the largest n_b (ignored when q_starts is NULL); tokens of
  *                 a sequence behind its max_q-th are left unwritten.
