@@ -6,9 +6,9 @@
 // load the reverse.  A block's scale needs the maximum over its rows before
 // the first code can be written, so a group of threads holds a whole run (at
 // most 64 rows of one head) in registers: one read of the input, one
-// reduction, one write.  Measured, 8 heads of 128: 40,007 tokens stored in 45
-// us (80% of the copy bandwidth; 512 threads a block 78, 8 blocks an SM 61),
-// 256 appended in 7.0; 65,536 loaded in 66 us (90%; keys and values by threads
+// reduction, one write.  Measured, 8 heads of 128: 40,007 tokens stored in 41
+// us (89% of the copy bandwidth; without the early prefetch of the rows 45, then
+// 512 threads a block 78, 8 blocks an SM 61), 256 appended in 6.8; 65,536 loaded in 66 us (90%; keys and values by threads
 // of their own 70).
 
 #include "fp4idx_attention_common.cuh"
@@ -133,6 +133,11 @@ __global__ __launch_bounds__(kStoreThreads) void kv_store_kernel(StoreArgs a, in
   const int64_t base = (int64_t)blockIdx.x * chunk;
   const int head = blockIdx.y;
   const StoreSide side = blockIdx.z ? a.v : a.k;
+  // the chunk's rows start on their way while the slots are looked at
+  constexpr int kLines = D / 64;
+  if (tid < chunk * kLines && base + tid / kLines < a.T)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(side.x + (base + tid / kLines) * side.tstride +
+                                                  head * side.hstride + tid % kLines * 64));
   if (tid < 2 * kPage) {
     int64_t s = -1, prev = -1;
     if (base + tid < a.T) {
