@@ -69,7 +69,8 @@ typedef struct fp4idx_kv_cache {
  *
  * A run is a set of consecutive tokens of the call whose slots are
  * consecutive and on one page.  For each run, head, and keys and values:
- *   amax  = max |x| over the run (NaN ignored);
+ *   amax  = max |x| over the run (NaN ignored; an infinity makes the scale
+ *           2^127, which leaves nothing of the page's other values);
  *   scale = ceil_pow2(max(rn32(amax / 448), 2^-126)), the rule of the FP8
  *           output mode of the pre-pass; if the run starts at an offset > 0,
  *           the page's rows before it are kept and scale is at least the
@@ -123,7 +124,9 @@ fp4idx_status fp4idx_kv_load_fp8(const fp4idx_kv_cache* cache, const int64_t* sl
  * The products of keys and queries are exact in the tensor core, the softmax
  * and both sums are fp32; probabilities are rounded to fp16 before the product
  * with the values, by 2^-11 of themselves or 2^-35 of the row's largest
- * contribution.
+ * contribution.  A score carries fp32's relative error into its exponent, so
+ * |x_s| is to stay below 2^20; of scores so large that their spacing exceeds
+ * the exponents' range, from about 2^23 on, the row's output is unspecified.
  *
  *   q             16-bit, row (t, h) at t*q_token_stride + h*q_head_stride
  *                 elements; 16-byte aligned, strides multiples of 8.  The
