@@ -24,21 +24,6 @@ int64_t item_rows(int64_t rows, int64_t head_dim) {
   return rows <= 8 ? 8 : rows <= 16 || head_dim == 128 ? 16 : 32;
 }
 
-// Whether items are cut where the CTAs' equal shares end, and joined, or each
-// is one CTA's.  Cutting saves what the fullest CTA has more than the mean: up
-// to one item's tiles, and where lengths differ perhaps a quarter of the rest.
-// It costs each CTA another item's start and end, the more the more rows, and
-// the join.  Measured, cut against whole, us: 8 items of 32 tiles 10.7 / 16.4,
-// 240 of 32 tiles 37 / 30, of 94 tiles 65 / 70, 160 of 63 tiles 40 / 43; 80 of
-// 32 rows and 32 tiles 62 / 39, 1024 of 16 rows and 128 tiles 338 / 380.
-// Selected tokens cost twice as much a tile, and their items are equal.
-bool worth_cutting(int64_t items, int64_t tiles, int64_t rows, bool sparse) {
-  const int64_t rounds = (items + kMaxGrid - 1) / kMaxGrid;
-  int64_t saved = (rounds * kMaxGrid - items) * tiles;  // tiles x CTAs
-  saved += sparse ? saved : items * tiles / 4;
-  return saved > (14 + rows) * rounds * kMaxGrid;
-}
-
 struct Workspace {
   int64_t part_lse, cuts, total;  // offsets in bytes; partial outputs at 0
 };
@@ -121,8 +106,11 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
 // `max_tiles`: 64-key tiles of an item, at most.
 fp4idx_status launch(AttnArgs& a, int head_dim, bool sparse, int64_t max_tiles, void* stream) {
   const int64_t items = (int64_t)a.batch * a.Hkv * a.rc_max;
-  // the tensor-core kernel always cuts
-  a.split = a.R == kTileRows || worth_cutting(items, max_tiles, a.R, sparse);
+  // The tensor-core kernel always cuts; the other one's dense form decides
+  // again by the lengths, of which the bound is taken for the longest here and
+  // the mean for less.
+  const int64_t total = sparse ? items * max_tiles : items * max_tiles * 3 / 4;
+  a.split = a.R == kTileRows || worth_cutting(items, total, max_tiles, a.R, kMaxGrid, sparse);
   const int64_t units = a.split ? items * max_tiles : items;
   const int grid = units < kMaxGrid ? (int)units : kMaxGrid;
   if (a.R == kTileRows)

@@ -200,20 +200,20 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   return m;
 }
 
-// The units of one item: its tiles, or the item as a whole.
-__device__ __forceinline__ int units_of(const AttnArgs& a, const Seq& m) {
-  return a.split ? m.nt : 1;
-}
-
 // A place in the list of items.
 template <bool kSparse>
 struct Cursor {
   int b, it;
   int64_t begin;  // the item's first unit
+  bool cut;       // units are tiles, or items as a whole (dense)
   Seq m;
 
+  __device__ __forceinline__ bool cuts(const AttnArgs& a) const {
+    return kSparse ? a.split != 0 : cut;
+  }
+  __device__ __forceinline__ int units(const AttnArgs& a) const { return cuts(a) ? m.nt : 1; }
   __device__ __forceinline__ void next(const AttnArgs& a) {
-    begin += units_of(a, m);
+    begin += units(a);
     if (++it == m.items) {
       it = 0;
       do {
@@ -225,10 +225,13 @@ struct Cursor {
 };
 
 // The units of the whole list, this CTA's share [s0, s1) of them and the
-// cursor at s0.  Dense: a prefix sum over the sequences, by the whole CTA.
+// cursor at s0.  Dense: a prefix sum over the sequences, by the whole CTA, and
+// the lengths decide whether items are cut after all, where the caller's bound
+// on them let it seem worth it (a.split).
 template <bool kSparse>
 __device__ __forceinline__ int64_t locate_share(const AttnArgs& a, Cursor<kSparse>& cur,
                                                 int64_t& s0, int64_t& s1) {
+  cur.cut = a.split != 0;
   const int cta = blockIdx.x;
   int64_t total = 0;
   // no CTA's share is empty but those behind the last unit's
@@ -239,7 +242,7 @@ __device__ __forceinline__ int64_t locate_share(const AttnArgs& a, Cursor<kSpars
   };
   if constexpr (kSparse) {
     cur.m = seq_of<true>(a, 0);
-    const int64_t per = (int64_t)cur.m.items * units_of(a, cur.m);
+    const int64_t per = (int64_t)cur.m.items * cur.units(a);
     total = per * a.batch;
     share();
     if (s0 >= s1) return total;
@@ -248,16 +251,41 @@ __device__ __forceinline__ int64_t locate_share(const AttnArgs& a, Cursor<kSpars
     cur.m = seq_of<true>(a, cur.b);
   } else {
     __shared__ int64_t part[kThreads / 32];
+    __shared__ int2 part_items[kThreads / 32];  // items; the longest one's tiles
     __shared__ int64_t found_begin;
     __shared__ int found_b;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int each = (a.batch + kThreads - 1) / kThreads;
     const int b0 = min(tid * each, a.batch), b1 = min(b0 + each, a.batch);
     int64_t own = 0;
+    int own_items = 0, most = 0;
     for (int b = b0; b < b1; ++b) {
       const Seq m = seq_of<false>(a, b);
-      own += (int64_t)m.items * units_of(a, m);
+      own += (int64_t)m.items * m.nt;
+      own_items += m.items;
+      if (m.items > 0) most = max(most, m.nt);
     }
+    if (a.split) {
+      most = __reduce_max_sync(kFull, most);
+      const int items = __reduce_add_sync(kFull, own_items);
+      int64_t sum = own;
+      for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(kFull, sum, d);
+      if (lane == 0) {
+        part[warp] = sum;
+        part_items[warp] = make_int2(items, most);
+      }
+      __syncthreads();
+      int n = 0;
+      int64_t tiles = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        tiles += part[w];
+        n += part_items[w].x;
+        most = max(most, part_items[w].y);
+      }
+      cur.cut = worth_cutting(n, tiles, most, a.R, gridDim.x, false);
+      __syncthreads();
+    }
+    if (!cur.cut) own = own_items;
     int64_t incl = own;
     for (int d = 1; d < 32; d *= 2) {
       const int64_t o = __shfl_up_sync(kFull, incl, d);
@@ -277,7 +305,7 @@ __device__ __forceinline__ int64_t locate_share(const AttnArgs& a, Cursor<kSpars
       int b = b0;
       for (;; ++b) {
         const Seq m = seq_of<false>(a, b);
-        const int64_t u = (int64_t)m.items * units_of(a, m);
+        const int64_t u = (int64_t)m.items * (cur.cut ? m.nt : 1);
         if (s0 < at + u) break;
         at += u;
       }
@@ -290,7 +318,7 @@ __device__ __forceinline__ int64_t locate_share(const AttnArgs& a, Cursor<kSpars
     cur.begin = found_begin;
     cur.m = seq_of<false>(a, cur.b);
   }
-  const int u = units_of(a, cur.m);
+  const int u = cur.units(a);
   cur.it = (int)((s0 - cur.begin) / u);
   cur.begin += (int64_t)cur.it * u;
   return total;
@@ -319,10 +347,10 @@ struct Producer {
   int f_idx, f_b, f_head;
 
   __device__ __forceinline__ void open(const AttnArgs& a, int64_t s1) {
-    const int u = units_of(a, pc.m);
+    const int u = pc.units(a);
     const int64_t end = min(s1, pc.begin + u);
-    t0 = a.split ? (int)(at - pc.begin) : 0;
-    xe = xb + 2 * (a.split ? (int)(end - at) : pc.m.nt);
+    t0 = pc.cuts(a) ? (int)(at - pc.begin) : 0;
+    xe = xb + 2 * (pc.cuts(a) ? (int)(end - at) : pc.m.nt);
     at = end;
   }
   __device__ __forceinline__ bool seek(const AttnArgs& a, int64_t s1) {
@@ -512,10 +540,10 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
   bool held = false;    // the slot before it is not released yet
   int xb = 0, x = warp;
   for (int64_t at = s0; at < s1;) {
-    const int u = units_of(a, cur.m);
+    const int u = cur.units(a);
     const int64_t end = min(s1, cur.begin + u);
-    const int t0 = a.split ? (int)(at - cur.begin) : 0;
-    const int xe = xb + 2 * (a.split ? (int)(end - at) : cur.m.nt);
+    const int t0 = cur.cuts(a) ? (int)(at - cur.begin) : 0;
+    const int xe = xb + 2 * (cur.cuts(a) ? (int)(end - at) : cur.m.nt);
     const int head = cur.it / cur.m.rcs;
     const int row0 = (cur.it - head * cur.m.rcs) * R;  // first row of the sequence's n * G
     const int rows = min(cur.m.n * a.G - row0, R);
