@@ -14,7 +14,7 @@ constexpr int kPage = FP4IDX_KV_BLOCK;
 // than kTileWork query rows x 64-key tiles in all.  Measured, the kernel for few
 // rows against it, us: 64 sequences x 8 key heads of 8192 keys, 32 rows 338 /
 // 323, 64 rows 660 / 324; of 500 keys and 500 tokens x 4 rows, 4 sequences x 2
-// key heads (900 row-tiles a CTA) 28 / 40, x 8 key heads (3700) 93 / 39.
+// key heads (840 row-tiles a CTA) 28 / 40, x 8 key heads (3370) 93 / 39.
 constexpr int64_t kTileFrom = 33;
 constexpr int64_t kTileWork = 1200 * kMaxGrid;
 constexpr int64_t kTileRows = 256;
