@@ -82,7 +82,7 @@ __host__ __device__ constexpr uint32_t smem_bytes(int D) {
 struct Item {
   int row0, rows;
   int q0, first;  // first query token of the sequence, its position
-  int hi;         // keys any row sees are below hi
+  int lo, hi;     // keys that any row sees: [lo, hi) and [0, sinks)
   int ts, tl;     // tiles: 0 .. ts-1, then tl ..
   int nt;         // tiles in all, at least one
 };
@@ -100,9 +100,8 @@ __device__ __forceinline__ bool item_of(const AttnArgs& a, int b, int rc, Item& 
   m.row0 = rc * kItemRows;
   m.rows = min(min(full, a.max_q) * a.G - m.row0, kItemRows);
   m.hi = max(min(ctx, m.first + (m.row0 + m.rows - 1) / a.G + 1), 0);
-  int lo = a.window > 0 ? max(m.first + m.row0 / a.G - a.window + 1, 0) : 0;
-  lo = min(lo, m.hi);
-  m.tl = lo / kTile;
+  m.lo = a.window > 0 ? min(max(m.first + m.row0 / a.G - a.window + 1, 0), m.hi) : 0;
+  m.tl = m.lo / kTile;
   m.ts = a.window > 0 ? min((a.sinks + kTile - 1) / kTile, m.tl) : 0;
   m.nt = max(m.ts + (m.hi + kTile - 1) / kTile - m.tl, 1);
   return m.rows > 0;
@@ -414,13 +413,17 @@ __device__ __forceinline__ int arrivals(int i) {
   return commit ? 1 : 4;
 }
 
-// A tile of the CTA's list, described ahead of its use.
+// A tile of the CTA's list, described ahead of its use.  A page that holds no
+// visible key (below the window, behind the first tokens) is not looked up, and
+// the rows that the item does not see are not loaded: zeros take their place,
+// since a probability of 0 times a NaN code is NaN.  (Two words a page: with
+// 64-bit masks the converters' tests took the prompts' 485 us to 496.)
 struct alignas(16) TileInfo {
-  float scale[4];  // ks of its two pages, vs of both (negative: page left out)
-  int64_t off[2];  // bytes from the codes' start to each page's rows of the head
-  int key0;        // its first key
-  int rows[2];     // rows of the pages that hold visible keys
-  int last;        // no tile follows
+  float scale[4];       // ks of its two pages, vs of both (negative: page left out)
+  int64_t off[2];       // bytes from the codes' start to each page's rows of the head
+  uint32_t rows[2][2];  // rows of each page that hold visible keys, a bit each
+  int key0;             // its first key
+  int last;             // no tile follows
 };
 
 struct Ctl {
@@ -713,7 +716,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
     const int cw = warp - kConvWarp;
     // the tile whose codes are loaded next
     int64_t off[2];
-    int rows[2];
+    uint32_t rows[2][2];
     bool last = false;
     const auto look = [&](uint32_t n) {
       const bool ok = 0 != __all_sync(kFull, wait_bar(bar(kTileFull + n % kTileRing),
@@ -723,7 +726,8 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         off[k] = info.off[k];
-        rows[k] = ok ? info.rows[k] : 0;
+        rows[k][0] = ok ? info.rows[k][0] : 0u;
+        rows[k][1] = ok ? info.rows[k][1] : 0u;
       }
       return ok;
     };
@@ -736,9 +740,10 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
     const auto load_k = [&]() {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int k = i / (kLoads / 2), row = key + i % (kLoads / 2) * (4 * kRows);
+        const int k = i / (kLoads / 2), step = i % (kLoads / 2) * (4 * kRows);
         kreg[i] = make_uint4(0, 0, 0, 0);
-        if (row < rows[k]) kreg[i] = ld_stream(a.kc + off[k] + row * D + c * 16);
+        if (rows[k][step / 32] & 1u << (key + step % 32))
+          kreg[i] = ld_stream(a.kc + off[k] + (key + step) * D + c * 16);
       }
     };
     // the lanes of the second column block store their upper half first: the
@@ -758,11 +763,13 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const uint8_t* src = a.vc + (page_of(i) ? off[1] : off[0]) + q * 4 * D + d0;
-        const int n = (page_of(i) ? rows[1] : rows[0]) - q * 4;
+        const uint32_t on0 = page_of(i) ? rows[1][0] : rows[0][0];
+        const uint32_t on1 = page_of(i) ? rows[1][1] : rows[0][1];
+        const uint32_t on = (q < 8 ? on0 : on1) >> (q % 8 * 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           vreg[i][j] = make_uint4(0, 0, 0, 0);
-          if (j < n) vreg[i][j] = ld_stream(src + j * D);
+          if (on >> j & 1u) vreg[i][j] = ld_stream(src + j * D);
         }
       }
     };
@@ -945,16 +952,21 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
           const int32_t* row = a.table + b * a.tstride + info.key0 / kPage;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            info.rows[e] = min(max(sg.m.hi - info.key0 - e * kPage, 0), kPage);
-            int page = info.rows[e] > 0 ? __ldg(row + e) : -1;
+            const int from = info.key0 + e * kPage;
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              info.rows[e][w] = sees(sg.m.hi - 1 - from - 32 * w, sg.m.lo - from - 32 * w,
+                                     a.sinks - from - 32 * w);
+            const bool seen = (info.rows[e][0] | info.rows[e][1]) != 0;
+            int page = seen ? __ldg(row + e) : -1;
             info.scale[e] = 1.0f;
             info.scale[2 + e] = -1.0f;
             if (page >= 0 && page < a.num_blocks) {
               info.scale[e] = a.ks[page * a.sstride + head];
               info.scale[2 + e] = fabsf(a.vs[page * a.sstride + head]);
             } else {
-              if (info.rows[e] > 0) flag_error(a.err, FP4IDX_ERRFLAG_PAGE);
-              info.rows[e] = page = 0;
+              if (seen) flag_error(a.err, FP4IDX_ERRFLAG_PAGE);
+              info.rows[e][0] = info.rows[e][1] = page = 0;
             }
             info.off[e] = page * a.cstride + (int64_t)head * kPage * D;
           }

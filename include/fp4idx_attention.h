@@ -153,8 +153,9 @@ fp4idx_status fp4idx_kv_load_fp8(const fp4idx_kv_cache* cache, const int64_t* sl
  *                 outside [0, num_blocks) (its keys are left out),
  *                 FP4IDX_ERRFLAG_TIMEOUT if a wait inside the kernel ran out.
  * A NaN code among the keys or values that one query of a sequence sees may
- * reach other queries of the sequence; bytes behind context_lens are never
- * used.
+ * reach other queries of the sequence.  What no query of the sequence sees
+ * (behind context_lens, below the window and behind the first tokens) is never
+ * used: its codes may hold anything, its pages' table entries too.
  */
 size_t fp4idx_attention_workspace_bytes(int64_t batch, int64_t max_q, int64_t num_heads,
                                         int64_t kv_heads, int64_t head_dim);
