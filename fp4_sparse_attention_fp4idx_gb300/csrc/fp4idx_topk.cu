@@ -4,8 +4,10 @@
 //
 // A logit becomes an unsigned key that orders like the float (0 for what can
 // never be selected).  One CTA per row, bound by reading the row once:
-//   1. 4,096 samples of the row give a threshold that about k + 4 sigma of
-//      its entries reach;
+//   1. 2,048 samples of the row (4,096 beyond 65,536 entries) give a threshold
+//      that about k + 4 sigma of its entries reach; where no more samples than
+//      that can be selected at all (a row mostly of -inf, as the scorer leaves
+//      those of a prompt's first tokens), every entry that can be reaches it;
 //   2. one pass over the row keeps the entries that reach it (a few
 //      thousand) with their places, in shared memory;
 //   3. the k-th largest of those is found exactly, 11 bits of the remaining
@@ -73,6 +75,7 @@ struct Shared {
   uint32_t part2[kWarps];
   uint32_t found[4];
   uint32_t lo, hi;   // least and largest key
+  uint32_t live;     // samples that can be selected
   uint32_t few[32];  // the keys of a bin of few
   uint32_t count;
 };
@@ -106,8 +109,9 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint3
   return part[warp] + incl - v;
 }
 
-// Of the bins' counts: the bin that holds the want-th largest (found[0]), the
-// number above it (found[1]) and in it (found[2]).
+// Of the bins' counts, which sum to `want` at least: the bin that holds the
+// want-th largest (found[0]), the number above it (found[1]) and in it
+// (found[2]).
 __device__ __forceinline__ void find_bin(uint32_t want, Shared& sh) {
   const int tid = threadIdx.x;
   // thread t sums the bins from the top: 4t .. 4t + 3 counted downwards
@@ -138,7 +142,8 @@ __device__ __forceinline__ void find_bin(uint32_t want, Shared& sh) {
 }
 
 // Narrows [lo, hi] to where the want-th largest key lies, by at most `passes`
-// histograms; keys outside [lo, hi] do not count.  On return the keys > hi
+// histograms; keys outside [lo, hi] do not count, and `want` at least lie
+// within.  On return the keys > hi
 // are all selected and `want` of those in [lo, hi] are; `in` is their number.
 // each(f): calls f for each of the thread's keys.
 template <typename Each>
@@ -167,7 +172,7 @@ __device__ __forceinline__ void narrow(const Each& each, uint32_t& lo, uint32_t&
       if (tid < 32) sh.few[tid] = 0;
       __syncthreads();
       each([&](uint32_t key) {
-        if (key >= lo && key <= hi) sh.few[atomicAdd(&sh.found[3], 1u)] = key;
+        if (key >= lo && key <= hi) sh.few[atomicAdd(&sh.found[3], 1u) % 32u] = key;
       });
       __syncthreads();
       if (tid < 32) {
@@ -372,6 +377,7 @@ __global__ __launch_bounds__(kThreads, kClustered ? 1 : 4) void topk_kernel(cons
   if (tid == 0) {
     sh.lo = kFull;
     sh.hi = 0;
+    sh.live = 0;
   }
 #pragma unroll
   for (int i = 0; i < kBins / kThreads; ++i) sh.bins[tid + i * kThreads] = 0;
@@ -396,25 +402,27 @@ __global__ __launch_bounds__(kThreads, kClustered ? 1 : 4) void topk_kernel(cons
       s[4 * i + 2] = key_of(w.z);
       s[4 * i + 3] = key_of(w.w);
     }
-    uint32_t smin = kFull, smax = 0;
+    uint32_t smin = kFull, smax = 0, live = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       smax = max(smax, s[i]);
       smin = min(smin, s[i] ? s[i] : kFull);
+      live += s[i] != 0;
     }
     smax = __reduce_max_sync(kFull, smax);
     smin = __reduce_min_sync(kFull, smin);
+    live = __reduce_add_sync(kFull, live);
     if (lane == 0) {
       atomicMax(&sh.hi, smax);
       atomicMin(&sh.lo, smin);
+      atomicAdd(&sh.live, live);
     }
     __syncthreads();
     smax = sh.hi;
     smin = sh.lo;
     const float p = (float)a.k / (float)n;
     uint32_t want = (uint32_t)(p * samples + 4.0f * sqrtf(p * (1.0f - p) * samples)) + 4u;
-    // more samples wanted than there are (few entries that count): all
-    if (p < 1.0f && want < (uint32_t)samples && smax != 0) {
+    if (want < sh.live) {  // else all: fewer samples can be selected than wanted
       uint32_t in = kFull;
       // by value, in equal steps: keys crowd into few bins, and lanes that
       // meet in a bin take turns
