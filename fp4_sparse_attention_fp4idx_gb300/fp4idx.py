@@ -14,6 +14,7 @@ Two layers:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -194,6 +195,16 @@ def _stream_ptr(stream):
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(int(s.cuda_stream))
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call makes its own allocations: on the stream that it runs on.
+    A fill is then in order with its kernel, and memory given back is used again
+    behind it."""
+    return _HERE if stream is None else _torch().cuda.stream(stream)
 
 
 def _need(t, dtype, name, ndim=None):
@@ -871,7 +882,7 @@ def kv_load_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, *, dtype=None,
                 v_out=None, err_flags=None, stream=None):
     """Reads cached tokens back -> (k, v) of `dtype` (bf16 by default, or
     fp16), [T, kv_heads, D].  A negative slot leaves its output row as it was
-    (zeros where the outputs are allocated here)."""
+    (zeros where the outputs are allocated here, on `stream`)."""
     torch = _torch()
     c, dev = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     _fits(slot_mapping, torch.int64, 1, dev, "slot_mapping")
@@ -881,10 +892,11 @@ def kv_load_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, *, dtype=None,
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else \
             v_out.dtype if v_out is not None else torch.bfloat16
-    if k_out is None:
-        k_out = torch.zeros(shape, device=k_cache.device, dtype=dtype)
-    if v_out is None:
-        v_out = torch.zeros(shape, device=k_cache.device, dtype=dtype)
+    with _on(stream):
+        if k_out is None:
+            k_out = torch.zeros(shape, device=k_cache.device, dtype=dtype)
+        if v_out is None:
+            v_out = torch.zeros(shape, device=k_cache.device, dtype=dtype)
     dt = _type16(k_out, "k_out")
     _fits(k_out, dtype, 3, dev, "k_out")
     _fits(v_out, dtype, 3, dev, "v_out")
