@@ -920,9 +920,9 @@ def _workspace_bytes(batch, max_q, num_heads, kv_heads, head_dim):
     return attention_workspace_bytes(batch, max_q, num_heads, kv_heads, head_dim) or 16
 
 
-def _attention_buffers(q, c, dev, block_table, out, lse, workspace, batch, max_q):
+def _attention_buffers(q, c, dev, block_table, out, lse, workspace, batch, max_q, stream):
     """Checks of q and block_table; (dtype code, strides of q, out, lse,
-    workspace), allocated where not given."""
+    workspace), allocated on `stream` where not given."""
     torch = _torch()
     dt = _type16(q, "q")
     H_kv, D = c.kv_heads, c.head_dim
@@ -934,23 +934,25 @@ def _attention_buffers(q, c, dev, block_table, out, lse, workspace, batch, max_q
     _fits(block_table, torch.int32, 2, dev, "block_table")
     if block_table.stride(1) != 1 and block_table.shape[1] > 1:
         raise ValueError("block_table must have unit column stride")
-    if out is None:
-        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, H, D))
-    else:
-        _fits(out, q.dtype, 3, dev, "out")
-        _dense(out, (T, H, D), "out")
-    device = out.device
-    if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=device)
-    else:
-        _fits(lse, torch.float32, 2, dev, "lse")
-        _dense(lse, (T, H), "lse")
-    if workspace is None:
-        workspace = torch.empty(_workspace_bytes(batch, max_q, H, H_kv, D), dtype=torch.uint8,
-                                device=device)
-    else:
-        _fits(workspace, torch.uint8, 1, dev, "workspace")
-        _dense(workspace, workspace.shape, "workspace")
+    device = q.device
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q) if q.is_contiguous() else \
+                torch.empty((T, H, D), dtype=q.dtype, device=device)
+        else:
+            _fits(out, q.dtype, 3, dev, "out")
+            _dense(out, (T, H, D), "out")
+        if lse is None:
+            lse = torch.empty((T, H), dtype=torch.float32, device=device)
+        else:
+            _fits(lse, torch.float32, 2, dev, "lse")
+            _dense(lse, (T, H), "lse")
+        if workspace is None:
+            workspace = torch.empty(_workspace_bytes(batch, max_q, H, H_kv, D), dtype=torch.uint8,
+                                    device=device)
+        else:
+            _fits(workspace, torch.uint8, 1, dev, "workspace")
+            _dense(workspace, workspace.shape, "workspace")
     return dt, qt, qh, out, lse, workspace
 
 
@@ -983,7 +985,7 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cont
             raise ValueError("without q_starts, T must be a multiple of the batch")
         max_q = T // batch if batch else 0
     dt, qt, qh, out, lse, workspace = _attention_buffers(q, c, dev, block_table, out, lse,
-                                                         workspace, batch, max_q)
+                                                         workspace, batch, max_q, stream)
     if block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, pages]")
     _call(_lib.fp4idx_paged_attention_fp8, dev, stream, q.data_ptr(), qt, qh, dt, ctypes.byref(c),
@@ -1012,7 +1014,7 @@ def sparse_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, ind
     if indices.shape[0] != T or (n > 1 and indices.stride(1) != 1):
         raise ValueError("indices must be [T, n] with unit column stride")
     dt, qt, qh, out, lse, workspace = _attention_buffers(q, c, dev, block_table, out, lse,
-                                                         workspace, T, 1)
+                                                         workspace, T, 1, stream)
     batch, pages = block_table.shape
     seqs = None
     if seq_ids is not None:

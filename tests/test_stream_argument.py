@@ -115,3 +115,18 @@ def test_load(F, monkeypatch):
     run(F, monkeypatch, lambda s: F.kv_load_fp8(*cache(), slots, stream=s), 2)
     one = gpu(torch.zeros(3, 2, 64, dtype=torch.bfloat16))
     run(F, monkeypatch, lambda s: F.kv_load_fp8(*cache(), slots, k_out=one, stream=s), 1)
+
+
+def test_attention(F, monkeypatch):
+    q = gpu(torch.zeros(2, 4, 64, dtype=torch.bfloat16))
+    packed = gpu(torch.zeros(2, 6, 64, dtype=torch.bfloat16))[:, 1:5]
+    table, lens = ints([0, 1], [2, 3]), ints(70, 5)
+    for x in (q, packed):
+        run(F, monkeypatch,
+            lambda s: F.paged_attention_fp8(x, *cache(), table, lens, 128, stream=s), 3)
+        run(F, monkeypatch,
+            lambda s: F.sparse_attention_fp8(x, *cache(), table, ints([0, 65, -1], [1, 2, 3]),
+                                             stream=s), 3)
+    out, lse = gpu(torch.zeros_like(q)), gpu(torch.zeros(2, 4))
+    run(F, monkeypatch, lambda s: F.paged_attention_fp8(q, *cache(), table, lens, 128, out=out,
+                                                        lse=lse, stream=s), 1)
