@@ -1048,17 +1048,18 @@ def topk_tokens(logits, k: int, *, row_lens=None, indices=None, counts=None, str
         _fits(row_lens, torch.int32, 1, dev, "row_lens")
         _dense(row_lens, (R,), "row_lens")
         lens = row_lens.data_ptr()
-    if indices is None:
-        indices = torch.empty((R, k), dtype=torch.int32, device=logits.device)
-    else:
-        _fits(indices, torch.int32, 2, dev, "indices")
-        if indices.shape != (R, k) or (k > 1 and indices.stride(1) != 1):
-            raise ValueError("indices must be [R, k] with unit column stride")
-    if counts is None:
-        counts = torch.empty((R,), dtype=torch.int32, device=logits.device)
-    else:
-        _fits(counts, torch.int32, 1, dev, "counts")
-        _dense(counts, (R,), "counts")
+    with _on(stream):
+        if indices is None:
+            indices = torch.empty((R, k), dtype=torch.int32, device=logits.device)
+        else:
+            _fits(indices, torch.int32, 2, dev, "indices")
+            if indices.shape != (R, k) or (k > 1 and indices.stride(1) != 1):
+                raise ValueError("indices must be [R, k] with unit column stride")
+        if counts is None:
+            counts = torch.empty((R,), dtype=torch.int32, device=logits.device)
+        else:
+            _fits(counts, torch.int32, 1, dev, "counts")
+            _dense(counts, (R,), "counts")
     _call(_lib.fp4idx_topk_tokens, dev, stream, logits.data_ptr(),
           logits.stride(0) if R > 1 else N, lens, indices.data_ptr(),
           indices.stride(0) if R > 1 else k, counts.data_ptr(), R, N, k)

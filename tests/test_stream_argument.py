@@ -130,3 +130,9 @@ def test_attention(F, monkeypatch):
     out, lse = gpu(torch.zeros_like(q)), gpu(torch.zeros(2, 4))
     run(F, monkeypatch, lambda s: F.paged_attention_fp8(q, *cache(), table, lens, 128, out=out,
                                                         lse=lse, stream=s), 1)
+
+
+def test_topk(F, monkeypatch):
+    x = gpu(torch.zeros(3, 50))
+    run(F, monkeypatch, lambda s: F.topk_tokens(x, 8, stream=s), 2)
+    run(F, monkeypatch, lambda s: F.topk_tokens(x, 1, counts=ints(0, 0, 0), stream=s), 1)

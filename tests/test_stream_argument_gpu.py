@@ -74,3 +74,21 @@ def test_workspace_is_not_taken_from_the_current_stream():
         torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_topk_beside_a_busy_current_stream():
+    """Memory that the current stream has given back but still writes does not
+    become the outputs of a call on another stream."""
+    x = torch.randn(64, 20000, device="cuda", generator=A.gen(5))
+    want = F().topk_tokens(x, 500)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        held = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (64 * 500, 64)]
+        torch.cuda._sleep(20_000_000)
+        for t in held:
+            t.fill_(7)
+        del held, t
+        got = F().topk_tokens(x, 500, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
