@@ -9,7 +9,8 @@ Two layers:
     and include/fp4idx_attention.h, plain integers for pointers).
   * torch wrappers with the same names (minus the ``fp4idx_`` prefix) that
     check dtypes/devices, allocate outputs with torch, pass ``data_ptr()``s
-    and the current CUDA stream, and raise ``Fp4idxError`` on a non-OK
+    and the current CUDA stream (or ``stream=``, on which outputs that are not
+    given are then allocated), and raise ``Fp4idxError`` on a non-OK
     status.  Every step of the computation runs in the library's kernels.
 """
 from __future__ import annotations
@@ -267,14 +268,15 @@ def k_norm_rope_pack_store(k, gamma, positions, cos_cache, sin_cache, slot_mappi
     _check(st, "fp4idx_k_norm_rope_pack_store")
 
 
-def _q_outputs(q_fp4, q_scale, weights, T, H, device):
+def _q_outputs(q_fp4, q_scale, weights, T, H, device, stream):
     torch = _torch()
-    if q_fp4 is None:
-        q_fp4 = torch.empty((T, H, 64), dtype=torch.uint8, device=device)
-    if q_scale is None:
-        q_scale = torch.empty((T, H, 4), dtype=torch.uint8, device=device)
-    if weights is None:
-        weights = torch.empty((T, H), dtype=torch.float32, device=device)
+    with _on(stream):
+        if q_fp4 is None:
+            q_fp4 = torch.empty((T, H, 64), dtype=torch.uint8, device=device)
+        if q_scale is None:
+            q_scale = torch.empty((T, H, 4), dtype=torch.uint8, device=device)
+        if weights is None:
+            weights = torch.empty((T, H), dtype=torch.float32, device=device)
     for t, shape, dt, name in ((q_fp4, (T, H, 64), torch.uint8, "q_fp4"),
                                (q_scale, (T, H, 4), torch.uint8, "q_scale"),
                                (weights, (T, H), torch.float32, "weights")):
@@ -311,7 +313,7 @@ def q_rope_pack_weights(q, w, positions, cos_cache, sin_cache, *, rope_style="ne
     """Queries -> (q_fp4 uint8 [T,H,64], q_scale uint8 [T,H,4], weights fp32
     [T,H]).  q bf16 [T,H,128] (strides multiples of 8), w bf16 [T,H]."""
     T, H = _check_q(q, w, positions, cos_cache, sin_cache)
-    q_fp4, q_scale, weights = _q_outputs(q_fp4, q_scale, weights, T, H, q.device)
+    q_fp4, q_scale, weights = _q_outputs(q_fp4, q_scale, weights, T, H, q.device, stream)
     ws = default_weight_scale(H) if weight_scale is None else float(weight_scale)
     args = (_ptr(q), q.stride(0), q.stride(1), _ptr(w), w.stride(0), ws, _ptr(positions),
             _ptr(cos_cache), _ptr(sin_cache), cos_cache.shape[0], rope_style_code(rope_style),
@@ -346,7 +348,7 @@ def indexer_prepass(k, gamma, slot_mapping, kv_cache, q, w, positions, cos_cache
         raise ValueError("slot_mapping must be contiguous [T]")
     if kv_cache.shape[1] != PAGE_BYTES or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be contiguous [num_blocks, 4352]")
-    q_fp4, q_scale, weights = _q_outputs(q_fp4, q_scale, weights, T, H, q.device)
+    q_fp4, q_scale, weights = _q_outputs(q_fp4, q_scale, weights, T, H, q.device, stream)
     ws = default_weight_scale(H) if weight_scale is None else float(weight_scale)
     args = (_ptr(k), k.stride(0), _ptr(gamma), float(eps), _ptr(slot_mapping), _ptr(kv_cache),
             kv_cache.shape[0], _ptr(q), q.stride(0), q.stride(1), _ptr(w), w.stride(0), ws,
@@ -537,7 +539,8 @@ def paged_mqa_logits(q_fp4, q_scale, weights, kv_cache, block_table, context_len
     if kv_cache.shape[1] != PAGE_BYTES or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be contiguous [num_blocks, 4352]")
     if logits is None:
-        logits = torch.empty((T, max_context), dtype=torch.float32, device=q_fp4.device)
+        with _on(stream):
+            logits = torch.empty((T, max_context), dtype=torch.float32, device=q_fp4.device)
     _need(logits, torch.float32, "logits", 2)
     if logits.shape[0] != T or logits.shape[1] < max_context or logits.stride(1) != 1:
         raise ValueError("logits must be [batch*next_n, >= max_context] with unit column stride")
@@ -580,7 +583,8 @@ def mqa_logits_prefill(q_fp4, q_scale, weights, kv_cache, ks, ke, num_keys: int,
     if kv_cache.shape[1] != PAGE_BYTES or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be contiguous [num_blocks, 4352]")
     if logits is None:
-        logits = torch.empty((T, num_keys), dtype=torch.float32, device=q_fp4.device)
+        with _on(stream):
+            logits = torch.empty((T, num_keys), dtype=torch.float32, device=q_fp4.device)
     _need(logits, torch.float32, "logits", 2)
     if logits.shape[0] != T or logits.shape[1] < num_keys or logits.stride(1) != 1:
         raise ValueError("logits must be [T, >= num_keys] with unit column stride")
@@ -616,12 +620,13 @@ def k_norm_rope_fp8_store(k, gamma, positions, cos_cache, sin_cache, slot_mappin
     _check(st, "fp4idx_k_norm_rope_pack_store_ex (FP8)")
 
 
-def _fp8_q_outputs(q_out, weights, T, H, device):
+def _fp8_q_outputs(q_out, weights, T, H, device, stream):
     torch = _torch()
-    if q_out is None:
-        q_out = torch.empty((T, H, HEAD_DIM), dtype=torch.uint8, device=device)
-    if weights is None:
-        weights = torch.empty((T, H), dtype=torch.float32, device=device)
+    with _on(stream):
+        if q_out is None:
+            q_out = torch.empty((T, H, HEAD_DIM), dtype=torch.uint8, device=device)
+        if weights is None:
+            weights = torch.empty((T, H), dtype=torch.float32, device=device)
     for t, shape, dt, name in ((q_out, (T, H, HEAD_DIM), torch.uint8, "q_out"),
                                (weights, (T, H), torch.float32, "weights")):
         _need(t, dt, name)
@@ -636,7 +641,7 @@ def q_rope_fp8_weights(q, w, positions, cos_cache, sin_cache, *, rope_style="neo
     """Queries -> (E4M3 codes uint8 [T,H,128], weights fp32 [T,H] with each
     row's power-of-two scale folded in)."""
     T, H = _check_q(q, w, positions, cos_cache, sin_cache)
-    q_out, weights = _fp8_q_outputs(q_out, weights, T, H, q.device)
+    q_out, weights = _fp8_q_outputs(q_out, weights, T, H, q.device, stream)
     ws = default_weight_scale(H) if weight_scale is None else float(weight_scale)
     opts = _options(1, hadamard, fp8=True)
     st = _lib.fp4idx_q_rope_pack_weights_ex(
@@ -662,7 +667,7 @@ def indexer_prepass_fp8(k, gamma, slot_mapping, kv_cache, q, w, positions, cos_c
         raise ValueError("kv_cache must be contiguous [num_blocks, 8448]")
     if k.shape[0] != T or k.shape[1] != HEAD_DIM or k.stride(1) != 1:
         raise ValueError("k must be [T,128] with unit element stride")
-    q_out, weights = _fp8_q_outputs(q_out, weights, T, H, q.device)
+    q_out, weights = _fp8_q_outputs(q_out, weights, T, H, q.device, stream)
     ws = default_weight_scale(H) if weight_scale is None else float(weight_scale)
     opts = _options(compress_ratio, hadamard, fp8=True)
     st = _lib.fp4idx_indexer_prepass_ex(
@@ -704,7 +709,8 @@ def rope_fake_quant(x, positions, cos_cache, sin_cache, *, rope_style="neox",
     if positions.shape[0] != T or not positions.is_contiguous():
         raise ValueError("positions must be contiguous [T]")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        with _on(stream):
+            out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
     _need(out, torch.bfloat16, "out")
     if tuple(out.shape) != tuple(x.shape) or not out.is_contiguous():
         raise ValueError("out must be contiguous with x's shape")

@@ -136,3 +136,39 @@ def test_topk(F, monkeypatch):
     x = gpu(torch.zeros(3, 50))
     run(F, monkeypatch, lambda s: F.topk_tokens(x, 8, stream=s), 2)
     run(F, monkeypatch, lambda s: F.topk_tokens(x, 1, counts=ints(0, 0, 0), stream=s), 1)
+
+
+def bf(*shape):
+    return gpu(torch.zeros(shape, dtype=torch.bfloat16))
+
+
+def longs(n):
+    return gpu(torch.zeros(n, dtype=torch.int64))
+
+
+@pytest.mark.parametrize("hadamard", [False, True])
+def test_prepass(F, monkeypatch, hadamard):
+    cos = gpu(torch.zeros(9, 32))
+    q, w, gamma = bf(2, 16, 128), bf(2, 16), bf(128)
+    pages, pages8 = (gpu(torch.zeros(3, n, dtype=torch.uint8)) for n in (4352, 8448))
+    kw = dict(hadamard=hadamard)
+    run(F, monkeypatch, lambda s: F.q_rope_pack_weights(
+        q, w, longs(2), cos, cos, stream=s, **kw), 3)
+    run(F, monkeypatch, lambda s: F.indexer_prepass(
+        bf(2, 128), gamma, longs(2), pages, q, w, longs(2), cos, cos, stream=s, **kw), 3)
+    run(F, monkeypatch, lambda s: F.q_rope_fp8_weights(
+        q, w, longs(2), cos, cos, stream=s, **kw), 2)
+    run(F, monkeypatch, lambda s: F.indexer_prepass_fp8(
+        bf(2, 128), gamma, longs(2), pages8, q, w, longs(2), cos, cos, stream=s, **kw), 2)
+
+
+def test_scorers_and_fake_quant(F, monkeypatch):
+    pages = gpu(torch.zeros(3, 4352, dtype=torch.uint8))
+    q4, qs = (gpu(torch.zeros(2, 32, n, dtype=torch.uint8)) for n in (64, 4))
+    wt = gpu(torch.zeros(2, 32))
+    run(F, monkeypatch, lambda s: F.paged_mqa_logits(
+        q4, qs, wt, pages, ints([0], [1]), ints(5, 6), 64, stream=s), 1)
+    run(F, monkeypatch, lambda s: F.mqa_logits_prefill(
+        q4, qs, wt, pages, ints(0, 0), ints(1, 2), 64, stream=s), 1)
+    run(F, monkeypatch, lambda s: F.rope_fake_quant(
+        bf(2, 128), longs(2), gpu(torch.zeros(9, 32)), gpu(torch.zeros(9, 32)), stream=s), 1)
