@@ -969,7 +969,8 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cont
     """Causal attention over the 8-bit cache -> (out [T, H, D] of q's dtype,
     lse fp32 [T, H]).  q bf16 or fp16 [T, H, D]; block_table int32 [batch,
     pages], context_lens int32 [batch] counts the query tokens too (their keys
-    and values are in the cache).  The query tokens are T / batch per sequence,
+    and values are in the cache); they are at most max_context, and that at most
+    pages * 64.  The query tokens are T / batch per sequence,
     or, with q_starts int32 [batch+1] and max_q (the longest), ragged.
     window > 0: a query sees the last `window` keys and the first `sinks`.
     softmax_scale defaults to D^-1/2."""
@@ -994,6 +995,9 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cont
                                                          workspace, batch, max_q, stream)
     if block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, pages]")
+    if T > 0 and block_table.shape[1] * KV_BLOCK < max_context:
+        # a view's rows go on behind its columns, so its stride says nothing
+        raise Fp4idxError(ERR_SHAPE, "fp4idx_paged_attention_fp8: max_context beyond block_table")
     _call(_lib.fp4idx_paged_attention_fp8, dev, stream, q.data_ptr(), qt, qh, dt, ctypes.byref(c),
           block_table.data_ptr(), block_table.stride(0) if batch > 1 else block_table.shape[1],
           context_lens.data_ptr(), starts, max_q, max_context, window, sinks,

@@ -65,7 +65,7 @@ class Library:
         self.lib, self.recorder = lib, recorder
 
     def __getattr__(self, name):
-        if name.endswith(("_bytes", "_scale")):
+        if name.endswith(("_bytes", "_scale", "_string")):
             return getattr(self.lib, name)
 
         def call(*args):
