@@ -54,9 +54,10 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
                           float softmax_scale, void* out, float* lse, int64_t items,
                           int64_t max_q, int64_t num_tokens, int64_t num_heads, void* workspace,
                           size_t workspace_bytes, uint32_t* err_flags, bool sparse,
-                          int64_t tiles) {
+                          int64_t tiles, bool no_pages) {
   const fp4idx_status cs = check_cache(cache);
-  if (cs == FP4IDX_ERR_NULL || !q || !block_table || !out || !workspace) return FP4IDX_ERR_NULL;
+  if (cs == FP4IDX_ERR_NULL || !q || (!block_table && !no_pages) || !out || !workspace)
+    return FP4IDX_ERR_NULL;
   if (cs == FP4IDX_ERR_SHAPE || num_heads < 1 || num_heads % cache->kv_heads ||
       num_tokens >= (1ll << 31) ||
       !workspace_args_ok(items, max_q, num_heads, cache->kv_heads, cache->head_dim))
@@ -164,7 +165,7 @@ extern "C" fp4idx_status fp4idx_paged_attention_fp8(
   const fp4idx_status st =
       common_args(a, q, q_token_stride, q_head_stride, dtype, cache, block_table,
                   block_table_stride, softmax_scale, out, lse, batch, max_q, num_tokens, num_heads,
-                  workspace, workspace_bytes, err_flags, false, tiles);
+                  workspace, workspace_bytes, err_flags, false, tiles, max_context == 0);
   if (st != FP4IDX_OK) return st;
   if (!aligned(context_lens, 4) || !aligned(q_starts, 4)) return FP4IDX_ERR_ALIGN;
   a.ctx = context_lens;
@@ -192,7 +193,8 @@ extern "C" fp4idx_status fp4idx_sparse_attention_fp8(
   const fp4idx_status st = common_args(a, q, q_token_stride, q_head_stride, dtype, cache,
                                        block_table, block_table_stride, softmax_scale, out, lse,
                                        num_tokens, 1, num_tokens, num_heads, workspace,
-                                       workspace_bytes, err_flags, true, 1);
+                                       workspace_bytes, err_flags, true, 1,
+                                       block_table_pages == 0);
   if (st != FP4IDX_OK) return st;
   if (!aligned(seq_ids, 4) || !aligned(indices, 4)) return FP4IDX_ERR_ALIGN;
   a.seq_ids = seq_ids;

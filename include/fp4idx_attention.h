@@ -133,7 +133,8 @@ fp4idx_status fp4idx_kv_load_fp8(const fp4idx_kv_cache* cache, const int64_t* sl
  *                 values are finite.
  *   block_table   int32, page p of sequence b at b*block_table_stride + p,
  *                 read for the pages that hold visible keys only;
- *                 block_table_stride >= ceil(max_context / 64).
+ *                 block_table_stride >= ceil(max_context / 64).  May be NULL
+ *                 where max_context is 0.
  *   context_lens  int32 [batch]; values are taken within [0, max_context].
  *   max_context   a bound on context_lens.  Kernel and work split are chosen
  *                 by it, so a loose one costs time, not correctness.
@@ -175,7 +176,7 @@ fp4idx_status fp4idx_paged_attention_fp8(
  * entry that occurs twice counts twice.  Everything else is as above.
  *
  *   block_table   int32, page p of sequence b at b*block_table_stride + p,
- *                 p < block_table_pages.
+ *                 p < block_table_pages.  May be NULL where that is 0.
  *   seq_ids       int32 [num_tokens], the sequence of each token, in
  *                 [0, batch); or NULL: token t belongs to sequence
  *                 t / (num_tokens / batch).
