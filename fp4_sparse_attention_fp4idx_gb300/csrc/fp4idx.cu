@@ -1179,6 +1179,8 @@ fp4idx_status fp4idx_test_withhold_next(int kernel, int64_t index) {
     fp4idx_impl::stream_withhold_next(index);
   else if (kernel == FP4IDX_TEST_SCORER)
     fp4idx_impl::scorer_withhold_next(index);
+  else if (kernel == FP4IDX_TEST_ATTENTION)
+    fp4idx_impl::attention_withhold_next(index);
   else
     return FP4IDX_ERR_ARG;
   return FP4IDX_OK;

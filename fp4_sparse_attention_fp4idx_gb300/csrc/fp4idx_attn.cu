@@ -104,8 +104,16 @@ fp4idx_status common_args(AttnArgs& a, const void* q, int64_t q_token_stride,
   return FP4IDX_OK;
 }
 
+// Testing hook: what the next launch withholds (-1: nothing), taken once.
+std::atomic<int64_t> g_attention_withhold{-1};
+
 // `max_tiles`: 64-key tiles of an item, at most.
 fp4idx_status launch(AttnArgs& a, int head_dim, bool sparse, int64_t max_tiles, void* stream) {
+  a.withhold = -1;
+  if (g_attention_withhold.load(std::memory_order_relaxed) >= 0) {
+    const int64_t w = g_attention_withhold.exchange(-1);
+    if (w < (1ll << 30)) a.withhold = (int32_t)w;
+  }
   const int64_t items = (int64_t)a.batch * a.Hkv * a.rc_max;
   // The tensor-core kernel always cuts; the other one's dense form decides
   // again by the lengths, of which the bound is taken for the longest here and
@@ -120,6 +128,9 @@ fp4idx_status launch(AttnArgs& a, int head_dim, bool sparse, int64_t max_tiles, 
 }
 
 }  // namespace
+
+void attention_withhold_next(int64_t index) { g_attention_withhold.store(index); }
+
 }  // namespace fp4idx_impl
 
 using namespace fp4idx_impl;

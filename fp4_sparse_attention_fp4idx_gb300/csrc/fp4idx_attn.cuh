@@ -35,6 +35,7 @@ struct AttnArgs {
   int32_t R;       // query rows of an item
   int32_t rc_max;  // row chunks of a sequence, at most
   int32_t split;   // items may be cut at tiles (partial outputs in the workspace)
+  int32_t withhold;  // testing: tile or stage of CTA 0 that is never ready (-1: none)
   float scale_log2;
   uint16_t* out;
   float* lse;

@@ -498,7 +498,8 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
   volatile uint32_t* const abort = &abort_flag;
 
   if (tid < kWarps * S) {  // 32 lanes' copies and the mask; the computing warp
-    mbar_init(bars + tid * 16, 33);
+    // (testing hook, see fp4idx_test_withhold_next: a stage that never fills)
+    mbar_init(bars + tid * 16, blockIdx.x == 0 && tid == a.withhold ? 34 : 33);
     mbar_init(bars + tid * 16 + 8, 1);
     fence_mbar_init();
   }

@@ -918,6 +918,8 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
     int64_t at = share.s0;
     int4 cut = make_int4(0, 0, 0, 0);
     uint32_t n = 0;  // tiles described
+    // (testing hook, see fp4idx_test_withhold_next: a tile that is not)
+    const int held = blockIdx.x == 0 ? a.withhold : -1;
     for (uint32_t i = 0; at < share.s1; ++i) {
       if (i >= kSegRing &&
           !__all_sync(kFull, wait_bar(bar(kSegEmpty + i % kSegRing), (i / kSegRing + 1) & 1u,
@@ -975,7 +977,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
           if (n >= kTileRing)
             ok = __all_sync(kFull, wait_bar(bar(kTileFree + n % kTileRing),
                                             (n / kTileRing + 1) & 1u, abort));
-          if (ok && lane == e) {
+          if (ok && lane == e && (int)n != held) {
             ctl.tiles[n % kTileRing] = info;
             mbar_arrive(bar(kTileFull + n % kTileRing));
           }
@@ -1002,8 +1004,9 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
   fence_before();
   __syncthreads();
   if (*abort) {
-    // MMAs in flight land before TMEM and shared memory are released
-    if (tid == kMmaWarp * 32) {
+    // MMAs in flight land before TMEM and shared memory are released.  A commit
+    // stands for its own lane's MMAs: the lane that was elected to issue them.
+    if (warp == kMmaWarp && elect_one()) {
       flag_error(a.err, FP4IDX_ERRFLAG_TIMEOUT);
       const uint32_t b = bar(kQFull);  // re-used: one arrival by the commit
       asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(b) : "memory");

@@ -346,10 +346,12 @@ bool stream_eligible(bool queries, int64_t H);
 fp4idx_status launch_stream(const KArgs& ka, const QArgs& qa, const Shared& sh, bool keys,
                             bool queries, int rope_style, int rotate, int fp8, void* stream);
 // The testing hook (fp4idx_test_withhold_next): the next launch of the
-// streaming kernel, or of a scorer, withholds the copies of work item `index`
-// of CTA 0 (a 64-row unit; a 128-key tile).
+// streaming kernel, of a scorer, or of an attention kernel, withholds the copies
+// of work item `index` of CTA 0 (a 64-row unit; a 128-key tile; a 128-key tile
+// or stage of a ring).
 void stream_withhold_next(int64_t index);
 void scorer_withhold_next(int64_t index);
+void attention_withhold_next(int64_t index);
 
 // The host-side checks of fp4idx_indexer_prepass(_ex) without the launch
 // (fp8: the FP8 output mode, where q_scale may be NULL).

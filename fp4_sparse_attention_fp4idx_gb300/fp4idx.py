@@ -166,12 +166,13 @@ def rope_style_code(style) -> int:
 
 TEST_PREPASS = 0
 TEST_SCORER = 1
+TEST_ATTENTION = 2
 
 
 def test_withhold_next(kernel: int, index: int) -> None:
     """Testing hook: the next launch of `kernel` (TEST_PREPASS: the streaming
-    pre-pass; TEST_SCORER: the scorers) leaves out the copies of work item
-    `index` of its first CTA, so its bounded waits run out (TIMEOUT flag)."""
+    pre-pass; TEST_SCORER: the scorers; TEST_ATTENTION: attention over the
+    8-bit cache) leaves out the copies of work item `index` of its first CTA, so its bounded waits run out (TIMEOUT flag)."""
     _check(_lib.fp4idx_test_withhold_next(int(kernel), int(index)), "fp4idx_test_withhold_next")
 
 

@@ -493,16 +493,18 @@ float fp4idx_default_weight_scale(int64_t num_heads);
  * next launch of the given kernel, on any thread, leaves out the copies of
  * one work item of its first CTA: a 64-row unit of the streaming pre-pass
  * kernel (FP4IDX_TEST_PREPASS; units count key units first, then query
- * units; head counts that are a multiple of 16), or a 128-key tile of the
+ * units; head counts that are a multiple of 16), a 128-key tile of the
  * scorers (FP4IDX_TEST_SCORER; tiles count in that CTA's order, and a tile's
- * partner in its stage pair is left out with it).  The waits for it then
- * run out after their 1 s limit: that launch raises FP4IDX_ERRFLAG_TIMEOUT,
- * leaves part of its outputs unwritten, drains its copies in flight and
- * returns; later launches are unaffected.  The hook is taken by that one
- * launch (an index past the CTA's work withholds nothing).  Returns
- * FP4IDX_ERR_ARG for an unknown kernel or a negative index.
+ * partner in its stage pair is left out with it), or of the attention kernels
+ * (FP4IDX_TEST_ATTENTION) a 128-key tile of the one for many rows, or a stage
+ * of the rings of the one for few.  The waits for it then run out after their
+ * 1 s limit: that launch raises FP4IDX_ERRFLAG_TIMEOUT, leaves part of its
+ * outputs unwritten or wrong, drains its copies in flight and returns; later
+ * launches are unaffected.  The hook is taken by that one launch (an index past
+ * the CTA's work withholds nothing).  Returns FP4IDX_ERR_ARG for an unknown
+ * kernel or a negative index.
  */
-enum { FP4IDX_TEST_PREPASS = 0, FP4IDX_TEST_SCORER = 1 };
+enum { FP4IDX_TEST_PREPASS = 0, FP4IDX_TEST_SCORER = 1, FP4IDX_TEST_ATTENTION = 2 };
 fp4idx_status fp4idx_test_withhold_next(int kernel, int64_t index);
 
 /* Static, NUL-terminated description of a status code. */
