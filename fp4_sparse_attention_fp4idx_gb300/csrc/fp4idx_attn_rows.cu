@@ -851,7 +851,7 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
     const int free_slot = slot == 0 ? S - 1 : slot - 1;
     __shared__ int free_of[kWarps];
     __shared__ float join_f[kWarps][R];  // factor of a warp's sums
-    __shared__ float join_s[2][R];       // of the row: the common factor; lse, log2
+    __shared__ float join_s[3][R];       // of the row: the common factors; lse, log2
     if (lane == 0) free_of[warp] = free_slot;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -900,8 +900,11 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
           for (int d = 1; d < kWarps; d *= 2) L += __shfl_xor_sync(kFull, L, d);
           join_f[w][r] = mw == -INFINITY ? 0.0f : exp2_approx(Mw - Mg);
           if (w == 0) {
-            join_s[0][r] = mg == -INFINITY ? 0.0f : __frcp_rn(L) * exp2_approx(Mg - mg - kShift);
+            // 2^(M-m-10) in two halves: with values near 2^-126 it is 0 itself
+            const float half = mg == -INFINITY ? 0.0f : exp2_approx(0.5f * (Mg - mg - kShift));
+            join_s[0][r] = mg == -INFINITY ? 0.0f : __frcp_rn(L) * half;
             join_s[1][r] = mg == -INFINITY ? -INFINITY : mg + __log2f(L);
+            join_s[2][r] = half;
           }
         }
         compute_sync();
@@ -923,11 +926,11 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
           o.z = fmaf(v.z, f, o.z);
           o.w = fmaf(v.w, f, o.w);
         }
-        const float f = join_s[0][r], lse2 = join_s[1][r];
-        o.x *= f;
-        o.y *= f;
-        o.z *= f;
-        o.w *= f;
+        const float f = join_s[0][r], lse2 = join_s[1][r], f2 = join_s[2][r];
+        o.x = o.x * f * f2;
+        o.y = o.y * f * f2;
+        o.z = o.z * f * f2;
+        o.w = o.w * f * f2;
         if (whole) {
           const int tok = cur.m.q0 + (row0 + r) / a.G;
           const int h = head * a.G + (row0 + r) % a.G;

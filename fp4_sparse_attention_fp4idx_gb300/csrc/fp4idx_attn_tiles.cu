@@ -673,7 +673,8 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
         fence_after();
         const bool some = mm != -INFINITY;
         const float inv = some ? __frcp_rn(l) : 0.0f;
-        const float f = some ? exp2_approx(MM - mm - kShift) : 0.0f;
+        // 2^(M-m-10) in two halves: with values near 2^-126 it is 0 itself
+        const float f = some ? exp2_approx(0.5f * (MM - mm - kShift)) : 0.0f;
         const float lse2 = some ? mm + __log2f(l) : -INFINITY;
         const int64_t orow = (int64_t)tok * a.Hq + h;
         const int64_t prow = (int64_t)part * kItemRows + half * kHalfRows + rl;
@@ -684,7 +685,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
           tmem_ld32(to + c, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * inv * f : 0.0f;
+          for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * (inv * f) * f : 0.0f;
           if (!live) {
           } else if (!whole) {
             float4* dst = reinterpret_cast<float4*>(a.part_out + prow * D + c);
