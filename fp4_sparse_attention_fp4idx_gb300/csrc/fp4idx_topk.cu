@@ -31,6 +31,8 @@
 
 #include <float.h>
 
+#include <algorithm>
+
 #include "fp4idx_attn.cuh"
 
 namespace fp4idx_impl {
@@ -42,9 +44,25 @@ constexpr int kBins = 2048;           // 11 bits
 constexpr int kMaxMapCols = 1 << 18;  // a bit map of 32 KB
 constexpr int kCluster = 8;
 
-// Candidates that fit.  The threshold lets through k + 4 sigma of the sampled
-// rank: about 1.6 k at k = 2048 of 65,536.
-constexpr int cap_of(int k) { return k <= 1024 ? 3200 : k * 9 / 4; }
+// Samples of a row of n entries.
+__host__ __device__ constexpr int samples_of(int n) { return (n > 65536 ? 8 : 4) * kThreads; }
+
+// Candidates that fit.  A sample stands for r entries, and the sampled rank is
+// w = k / r + 4 sqrt(k / r) + 4, so about w r entries reach the threshold, 1.6 k at
+// k = 2048 of 65,536.  More than C do if fewer than w samples lie among the C
+// largest, of which C / r are expected with a deviation of sqrt(C / r): C is
+// taken where w is four deviations below, since a row with more takes the
+// general method, 7 to 40 times as long.  (9/4 k alone is up to two deviations
+// from k = 1025 on: 512 rows of 65,536 took 248 us at k = 1100, 35 at 1024; 64 of
+// 262,144 took 785 at k = 2048, now 35.)
+constexpr int kMaxCap = 9600;
+int cap_of(int k, int cols) {
+  int r = (cols + samples_of(cols) - 1) / samples_of(cols);
+  if (cols > 65536 && r < 32) r = 32;  // a row may be shorter
+  const double w = (double)k / r + 4 * sqrt((double)k / r) + 4;
+  const int most = (int)(r * (w + 8 + 4 * sqrt(w + 4)));
+  return std::min(kMaxCap, std::max(most, std::max(3200, k * 9 / 4)));
+}
 
 struct TopkArgs {
   const float* logits;
@@ -386,8 +404,8 @@ __global__ __launch_bounds__(kThreads, kClustered ? 1 : 4) void topk_kernel(cons
     // ---- the threshold: the sample of rank k/n * samples + 4 sigma.  Groups
     // of 8 neighbours, a lane four of them: a load that meets 32 lines holds
     // the L1 for as many cycles.
-    const bool twice = n > 65536;
-    const int samples = twice ? 8 * kThreads : 4 * kThreads;
+    const int samples = samples_of(n);
+    const bool twice = samples > 4 * kThreads;
     const int head = (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) / 4 % 4);
     const float4* xv = reinterpret_cast<const float4*>(x + head);
     const int groups = (n - head) / 4 - 1;  // a group may begin at any of these words
@@ -563,14 +581,14 @@ extern "C" fp4idx_status fp4idx_topk_tokens(const float* logits, int64_t logits_
     return FP4IDX_ERR_ALIGN;
   TopkArgs a = {logits, logits_stride, row_lens, indices, indices_stride, counts,
                 (int32_t)num_cols, (int32_t)k, 0, 0};
-  a.cap = cap_of(a.k);
+  a.cap = cap_of(a.k, a.cols);
   size_t bytes = 0;
   bool clustered = false;
   if (num_cols <= kMaxMapCols) {
     a.map_words = (int32_t)((num_cols + 31) / 32);
     if (a.map_words == 0) a.map_words = 1;
     bytes = (2 * (size_t)a.cap + (a.map_words <= kBins ? 1 : 2) * a.map_words) * 4;
-    constexpr int most = (2 * cap_of(4096) + 2 * kMaxMapCols / 32) * 4;
+    constexpr int most = (2 * kMaxCap + 2 * kMaxMapCols / 32) * 4;
     static SmemOnce once, once_clustered;
     if (!once.set(topk_kernel<false>, most) || !once_clustered.set(topk_kernel<true>, most))
       return FP4IDX_ERR_CUDA;
