@@ -12,9 +12,14 @@ constexpr int kPage = FP4IDX_KV_BLOCK;
 // The tensor-core kernel of 256-row items (fp4idx_attn_tiles.cu) takes dense
 // calls of at least kTileFrom query rows per sequence and key head and of more
 // than kTileWork query rows x 64-key tiles in all.  Measured, the kernel for few
-// rows against it, us: 64 sequences x 8 key heads of 8192 keys, 32 rows 338 /
-// 323, 64 rows 660 / 324; of 500 keys and 500 tokens x 4 rows, 4 sequences x 2
-// key heads (840 row-tiles a CTA) 28 / 40, x 8 key heads (3370) 93 / 39.
+// rows against it, us, 8 key heads; D = 128, sequences of up to 8192 keys: 16 rows
+// 181 / 322, 24 rows 328 / 323, 32 rows 339 / 325, 64 rows 660 / 324; 32 rows of
+// 64 sequences x 2048 keys 131 / 135, of 16 x 8192 132 / 120, of 16 x 32768 274 /
+// 303; D = 64, 32 rows, the same four: 213 / 252, 84 / 101, 84 / 92, 168 / 242; a
+// window of 4096 + 4, 48 sequences x 4 key heads, D = 64 76 / 90, D = 128 97 / 114.
+// Up to 32 rows the first loses 5 to 10% at most and wins up to twice that.
+// Of 500 keys and 500 tokens x 4 rows, 4 sequences x 2 key heads (840 row-tiles a
+// CTA) 28 / 40, x 8 key heads (3370) 93 / 39.
 constexpr int64_t kTileFrom = 33;
 constexpr int64_t kTileWork = 1200 * kMaxGrid;
 constexpr int64_t kTileRows = 256;

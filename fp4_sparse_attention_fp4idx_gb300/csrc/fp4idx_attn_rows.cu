@@ -12,14 +12,17 @@
 // with asynchronous copies: the walk over pages or selected entries and the
 // copies' issue took a computing warp 950 to 1,900 cycles a piece, next to
 // 1,450 to 2,500 of arithmetic.  Measured: 64 single tokens, 8 key heads of
-// 128, contexts up to 32,768, 430 us (90% of the copy bandwidth); 32 rows, 192
-// items of 65 tiles, heads of 64, 76 us (a piece takes a warp 3,800 cycles);
-// 64 tokens of 2,048 selected keys each 69 us, 1,021 over one key head 133.
+// 128, contexts up to 32,768, 428 to 448 us box to box (87 to 91% of the copy
+// bandwidth); 32 rows, 192 items of 65 tiles, heads of 64, 76 us (a piece takes
+// a warp 3,800 cycles); 64 tokens of 2,048 selected keys each 69 us, 1,021 over
+// one key head 134.
 //
 // Mathematics.  Codes are E4M3, exact in fp16; a query row is scaled by a
-// power of two into fp16's range, exact for bf16 and fp16 elements down to
-// 2^-38 of the row's largest, so the products of the score are exact and their
-// sum is fp32.  With the page's scales ks and vs (powers of two), in units of
+// power of two, its largest element into [2^14, 2^15).  That is exact for bf16
+// elements down to 2^-31 of the largest and for fp16 ones down to 2^-28 (8 and 11
+// bits above fp16's least step of 2^-24); smaller ones are rounded by 2^-39 of
+// the largest at most.  The products of the score are exact and their sum is
+// fp32.  With the page's scales ks and vs (powers of two), in units of
 // log2:  s = sum(q k) * ks * scale * log2(e).  The running softmax has two
 // references: m, of the sum l = sum 2^(s-m), and M, of the output sums,
 //   p = 2^(s + log2 vs - M + 10) in fp16,   O = sum p * code,

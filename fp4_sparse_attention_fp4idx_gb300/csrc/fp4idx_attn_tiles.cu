@@ -6,9 +6,10 @@
 // What bounds it.  4 D operations per query row and key against 2 D bytes per
 // key for a whole item of 256 rows: the tensor cores, then the exponentials.
 // Measured: 4 chunks of up to 1,500 tokens, 32 heads of 128 over 8 key heads,
-// contexts up to 16,384, 481 us, 55% of the bf16 rate; a tile takes about 2,850
-// cycles, its MMAs 2,051, a half's own chain of scores, softmax and product
-// the rest of it.
+// contexts up to 16,384, 486 us, 55% of the bf16 rate.  That is 4,800 cycles for
+// each of a CTA's 210 tiles at 2,070 MHz, segments' starts and ends among them;
+// the MMAs of a tile alone take 2,051, a half's softmax 1,222 to 1,706.  (Where
+// the rest goes is not measured; the tensor pipe is busy 45% of the time.)
 //
 // Mathematics.  As in fp4idx_attn_rows.cu: E4M3 codes are exact in fp16 and a
 // query row is scaled by a power of two into fp16's range (with the sign of
