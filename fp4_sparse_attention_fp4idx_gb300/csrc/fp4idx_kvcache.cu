@@ -7,7 +7,7 @@
 // the first code can be written, so a group of threads holds a whole run (at
 // most 64 rows of one head) in registers: one read of the input, one
 // reduction, one write.  Measured, 8 heads of 128: 40,007 tokens stored in 41
-// us (89% of the copy bandwidth; without the early prefetch of the rows 45, then
+// us (88% of the copy bandwidth; without the early prefetch of the rows 45, then
 // 512 threads a block 78, 8 blocks an SM 61), 256 appended in 6.8; 65,536 loaded in 66 us (90%; keys and values by threads
 // of their own 70).
 
