@@ -964,8 +964,9 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(const AttnArgs a) {
 }
 
 // Joins the partial outputs of the items that a share's end cut: weights
-// 2^(lse - max lse), in the order of the CTAs.  One block per CTA whose share
-// begins such an item, a warp per row.
+// 2^(lse - max lse), in the order of the CTAs, applied in two halves (a part of
+// weight 2^-126 counts where its values are as much larger).  One block per CTA
+// whose share begins such an item, a warp per row.
 template <int D, bool kSparse>
 __global__ __launch_bounds__(128) void join_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -991,11 +992,11 @@ __global__ __launch_bounds__(128) void join_kernel(const AttnArgs a) {
 #pragma unroll 4
       for (int f = 0; f < n; ++f) {
         const int64_t slot = (int64_t)(f == 0 ? first : 2 * (cta + f)) * a.R + r;
-        const float w = exp2_approx(a.part_lse[slot] - top);
-        den += w;
+        const float half = exp2_approx(0.5f * (a.part_lse[slot] - top));
+        den = fmaf(half, half, den);
         const float* p = a.part_out + slot * D + lane * kV;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) o[i] = fmaf(p[i], w, o[i]);
+        for (int i = 0; i < kV; ++i) o[i] = fmaf(p[i] * half, half, o[i]);
       }
       const float inv = __frcp_rn(den);
 #pragma unroll

@@ -1029,8 +1029,9 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
 }
 
 // Joins the partial outputs of the items that a share's end cut: weights
-// 2^(lse - max), in the order of the CTAs.  Blocks (CTA whose share begins the
-// item, 32 of its rows), four rows a warp.
+// 2^(lse - max), in the order of the CTAs, applied in two halves (a part of weight
+// 2^-126 counts where its values are as much larger).  Blocks (CTA whose share
+// begins the item, 32 of its rows), four rows a warp.
 template <int D>
 __global__ __launch_bounds__(256) void join_tiles_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1065,10 +1066,11 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(const AttnArgs a) {
     for (int k = 0; k < kRows; ++k) {
       if (r0 + k >= m.rows || top[k] == -INFINITY) continue;
       const int64_t row = slot(f) * kItemRows + r0 + k;
-      const float w = exp2_approx(a.part_lse[row] - top[k]);
-      den[k] += w;
+      const float half = exp2_approx(0.5f * (a.part_lse[row] - top[k]));
+      den[k] = fmaf(half, half, den[k]);
 #pragma unroll
-      for (int j = 0; j < kV; ++j) o[k][j] = fmaf(a.part_out[row * D + lane * kV + j], w, o[k][j]);
+      for (int j = 0; j < kV; ++j)
+        o[k][j] = fmaf(a.part_out[row * D + lane * kV + j] * half, half, o[k][j]);
     }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
