@@ -1169,7 +1169,7 @@ const char* fp4idx_status_string(fp4idx_status status) {
   return "unknown status";
 }
 
-const char* fp4idx_version(void) { return "fp4idx 0.5.0 sm_103a"; }
+const char* fp4idx_version(void) { return "fp4idx 0.6.0 sm_103a"; }
 
 // H^-1/2 * D^-1/2 with D = 128, evaluated in double and rounded once to fp32;
 // 0 for a non-positive head count.
@@ -1181,6 +1181,8 @@ fp4idx_status fp4idx_test_withhold_next(int kernel, int64_t index) {
     fp4idx_impl::scorer_withhold_next(index);
   else if (kernel == FP4IDX_TEST_ATTENTION)
     fp4idx_impl::attention_withhold_next(index);
+  else if (kernel == FP4IDX_TEST_PROMPT)
+    fp4idx_impl::prompt_withhold_next(index);
   else
     return FP4IDX_ERR_ARG;
   return FP4IDX_OK;

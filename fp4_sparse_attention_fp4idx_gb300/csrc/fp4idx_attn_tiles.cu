@@ -51,6 +51,7 @@
 #include <type_traits>
 
 #include "fp4idx_attn.cuh"
+#include "fp4idx_tc.cuh"
 
 namespace fp4idx_impl {
 namespace {
@@ -200,136 +201,9 @@ __device__ __forceinline__ int cta_of(int64_t x, const Share& sh) {
   return (int)(((x + 1) * sh.grid - 1) / sh.total);
 }
 
-// Waits for a phase; false when another role has given up or after 1 s.  The
-// clock is read seldom: a read of it costs more than most waits take.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
-  unsigned long long t0 = 0;
-  for (;;) {
-#pragma unroll 1
-    for (int k = 0; k < 256; ++k)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    const unsigned long long now = global_ns();
-    if (t0 == 0) {
-      t0 = now;
-    } else if (now - t0 > kWaitLimitNs) {
-      *abort = 1u;
-      return false;
-    }
-  }
-}
-
-// K-major operand in the 128-byte swizzled layout: rows of 128 bytes, 8-row
-// groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
-  uint64_t d = (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
 // kind::f16: fp16 A and B, both K-major, fp32 D, M = 128.
 __host__ __device__ constexpr uint32_t f16_idesc(int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kHalfRows >> 4) << 24);
-}
-
-// The MMAs and commits take the elected lane as a predicate: the whole warp
-// computes their operands, which then live in uniform registers.
-__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint64_t a, uint64_t b,
-                                       uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a, uint64_t b,
-                                       uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t elected, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "setp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          bar),
-      "r"(elected)
-      : "memory");
-}
-
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r;
-}
-
-__device__ __forceinline__ void fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// 32 columns of the thread's lane, as fp32.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
-        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
-        "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]),
-        "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]),
-        "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
-        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
-        "=f"(r[14]), "=f"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
@@ -339,52 +213,8 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// The largest of 32 values, two to an instruction in four chains.
-__device__ __forceinline__ float top32(const float* s) {
-  float x[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-  for (int i = 4; i < 28; i += 8)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = max3(x[j], s[i + 2 * j], s[i + 2 * j + 1]);
-  return max3(max3(x[0], s[28], s[29]), max3(x[1], s[30], s[31]), fmaxf(x[2], x[3]));
-}
-
-// (a * b + c, a' * b + c) packed.
-__device__ __forceinline__ void fma2s(float& r0, float& r1, float a0, float a1, float b, float c) {
-  asm("{\n\t.reg .b64 ra, rb, rc, rr;\n\t"
-      "mov.b64 ra, {%2, %3};\n\t"
-      "mov.b64 rb, {%4, %4};\n\t"
-      "mov.b64 rc, {%5, %5};\n\t"
-      "fma.rn.f32x2 rr, ra, rb, rc;\n\t"
-      "mov.b64 {%0, %1}, rr;\n\t}"
-      : "=f"(r0), "=f"(r1)
-      : "f"(a0), "f"(a1), "f"(b), "f"(c));
-}
-
 __device__ __forceinline__ float log2_scale(float s) {
   return (float)((int)(__float_as_uint(s) >> 23 & 0xffu) - 127);
-}
-
-__device__ __forceinline__ float or_zero(float m) { return m == -INFINITY ? 0.0f : m; }
-
-// Bits i of a word with i <= last.
-__device__ __forceinline__ uint32_t bits_to(int last) {
-  return last >= 31 ? kFull : last < 0 ? 0u : (2u << last) - 1u;
-}
-
-// The keys that a row sees of 32 of a tile's: key i (from the first of the 32)
-// with i <= hi and (i >= lo or i < sk).
-__device__ __forceinline__ uint32_t sees(int hi, int lo, int sk) {
-  return bits_to(hi) & (~bits_to(lo - 1) | bits_to(sk - 1));
-}
-
-template <int N>
-__device__ __forceinline__ void set_regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void set_regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Barriers.
@@ -1028,10 +858,8 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
   }
 }
 
-// Joins the partial outputs of the items that a share's end cut: weights
-// 2^(lse - max), in the order of the CTAs, applied in two halves (a part of weight
-// 2^-126 counts where its values are as much larger).  Blocks (CTA whose share
-// begins the item, 32 of its rows), four rows a warp.
+// Joins the partial outputs of the items that a share's end cut (join_rows).
+// Blocks (CTA whose share begins the item, 32 of its rows), four rows a warp.
 template <int D>
 __global__ __launch_bounds__(256) void join_tiles_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1048,30 +876,7 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(const AttnArgs a) {
   const int r0 = blockIdx.x % kBlocks * 32 + threadIdx.x / 32 * kRows;
   if (r0 >= m.rows) return;
   float top[kRows], den[kRows], o[kRows][kV];
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    top[k] = -INFINITY;
-    den[k] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kV; ++j) o[k][j] = 0.0f;
-  }
-#pragma unroll 2
-  for (int f = 0; f < n; ++f)
-#pragma unroll
-    for (int k = 0; k < kRows; ++k)
-      if (r0 + k < m.rows) top[k] = fmaxf(top[k], a.part_lse[slot(f) * kItemRows + r0 + k]);
-#pragma unroll 2
-  for (int f = 0; f < n; ++f)
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      if (r0 + k >= m.rows || top[k] == -INFINITY) continue;
-      const int64_t row = slot(f) * kItemRows + r0 + k;
-      const float half = exp2_approx(0.5f * (a.part_lse[row] - top[k]));
-      den[k] = fmaf(half, half, den[k]);
-#pragma unroll
-      for (int j = 0; j < kV; ++j)
-        o[k][j] = fmaf(a.part_out[row * D + lane * kV + j] * half, half, o[k][j]);
-    }
+  join_rows<D, kRows, kItemRows>(a.part_out, a.part_lse, n, r0, m.rows, lane, slot, top, den, o);
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     const int r = m.row0 + r0 + k;

@@ -348,10 +348,11 @@ fp4idx_status launch_stream(const KArgs& ka, const QArgs& qa, const Shared& sh, 
 // The testing hook (fp4idx_test_withhold_next): the next launch of the
 // streaming kernel, of a scorer, or of an attention kernel, withholds the copies
 // of work item `index` of CTA 0 (a 64-row unit; a 128-key tile; a 128-key tile
-// or stage of a ring).
+// or stage of a ring; for prompts the keys of a 128-key tile).
 void stream_withhold_next(int64_t index);
 void scorer_withhold_next(int64_t index);
 void attention_withhold_next(int64_t index);
+void prompt_withhold_next(int64_t index);
 
 // The host-side checks of fp4idx_indexer_prepass(_ex) without the launch
 // (fp8: the FP8 output mode, where q_scale may be NULL).

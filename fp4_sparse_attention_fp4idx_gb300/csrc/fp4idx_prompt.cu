@@ -1,0 +1,986 @@
+// fp4idx_prompt.cu -- attention of packed sequences over their own keys and
+// values in 16 bits (fp4idx_prompt_attention, defined in include/fp4idx_step.h),
+// on the tensor cores through tcgen05.mma kind::f16.
+//
+// What bounds it.  4 D operations per query row and key against 4 D bytes per
+// key for a whole item of 256 rows: the tensor cores and, next to them, one
+// exponential per score; for single tokens over long keys the keys' bytes.
+//
+// Mathematics.  With x = softmax_scale * log2(e) * q k a row keeps M, the
+// reference of its sums, l = sum 2^(x - M + shift) and O = sum 2^(x - M + shift) v;
+// out = O / l.  M follows the largest x only when that has grown by more than
+// kSlack, so the sums in TMEM are seldom rescaled.  Probabilities are rounded to
+// the elements' type for the product with the values (the tensor core wants both
+// operands of one type): bf16 keeps fp32's range, and 2^8 is as far as one may
+// exceed M; in fp16 they are shifted up by 2^10 and may grow by 2^4 more, so that
+// the smallest that does not vanish is 2^-35 of the largest.  l is summed from
+// the unrounded ones.
+//
+// Roles (one CTA per SM).  An item is 256 rows (token i, head g of a key head's
+// group: row i * G + g) of a sequence, as two M = 128 halves A and B that share
+// every key tile of 128 keys.
+//   warp 0          issues the MMAs: S = Q K^T, then O += P V with P from TMEM
+//                   and V as it lies in memory (the transposed operand form).
+//                   While half A's softmax runs, half B's products do.
+//   warp 1          walks the CTA's list of work, describes its segments and
+//                   loads their key and value tiles by TMA, 128-byte swizzled,
+//                   into a ring that keys and values share
+//   warps 2, 3      queries of half A, of half B, into shared memory; and rows
+//                   of a value tile that no query of the item sees are set to
+//                   zero (a probability of 0 times what may lie there is NaN)
+//   warps 4-7, 8-11 softmax of half A, of half B: a row per thread, its 128
+//                   scores read from TMEM into registers, its probabilities
+//                   written back over the first half of them
+// TMEM: scores A and B at columns 0 and 128 (P over the first 64), O at 256 and
+// 256 + D.
+// The items and their tiles form one list, cut into equal shares, one per CTA,
+// from the lengths alone; an item cut by a share's end leaves normalised
+// partial outputs, joined by a second kernel in a fixed order.
+// Every wait is bounded (1 s) and a shared abort flag stops every role; copies
+// and MMAs in flight are waited for before the CTA ends.
+
+#include <cuda.h>
+
+#include "fp4idx_attn.cuh"
+#include "fp4idx_step.h"
+#include "fp4idx_tc.cuh"
+
+namespace fp4idx_impl {
+namespace {
+
+constexpr int kTile = 128;  // keys of a tile
+constexpr int kHalfRows = 128;
+constexpr int kItemRows = 2 * kHalfRows;
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kSideWarp = 2, kSoftWarp = 4;
+constexpr int kThreads = 12 * 32;
+constexpr int kSegUsers = 11;  // warps that read a segment: the issuer, the sides, the softmax
+constexpr int kSegRing = 2;
+constexpr int kCleanRing = 4;
+// Registers of a thread, by warpgroup, within the launch's 168.
+constexpr int kLaunchRegs = 168, kSoftRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftRegs + kOtherRegs <= 3 * kLaunchRegs, "the launch's registers");
+constexpr uint32_t kTmemCols = 512;
+
+__host__ __device__ constexpr uint32_t q_bytes(int D) { return kItemRows * D * 2; }
+__host__ __device__ constexpr uint32_t kv_bytes(int D) { return kTile * D * 2; }
+// Tiles of keys and values in shared memory.
+__host__ __device__ constexpr int ring_of(int D) { return D == 128 ? 5 : 8; }
+// A value tile's clean barrier is used again 4 tiles on, its own slot 4 at most.
+static_assert(ring_of(64) <= 2 * kCleanRing && ring_of(128) <= 2 * kCleanRing, "clean ring");
+__host__ __device__ constexpr uint32_t smem_bytes(int D) {
+  return q_bytes(D) + ring_of(D) * kv_bytes(D) + 1024;
+}
+
+struct PromptArgs {
+  CUtensorMap kmap, vmap;
+  int32_t kx, kz, vx, vz;  // a head's step in the maps' first and last coordinate
+  const uint16_t* q;
+  int64_t q_ts, q_hs;
+  const int32_t* q_starts;
+  const int32_t* k_starts;
+  int32_t max_q, max_k, window, sinks;
+  int32_t batch, Tq, Tk, Hq, Hkv, G;
+  FastDiv by_g;
+  int32_t rc_max;    // row chunks of a sequence, at most
+  int32_t withhold;  // testing: tile of CTA 0 that is never loaded (-1: none)
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  float* part_out;  // [slot][kItemRows][D] normalised partial outputs
+  float* part_lse;  // [slot][kItemRows], log2
+  // [grid]: the item that begins in a CTA's share and ends in another's:
+  // sequence, row chunk, key head, CTAs * 2 + the first one's slot (0: none)
+  int4* cuts;
+  uint32_t* err;
+};
+
+// One item: up to 256 consecutive rows of a sequence and key head.
+struct Item {
+  int row0, rows;
+  int q0, k0;     // first query token and first key of the sequence
+  int first;      // position of its first query token
+  int lo, hi;     // keys that any row sees: [lo, hi) and [0, sinks)
+  int ts, tl;     // tiles: 0 .. ts-1, then tl ..
+  int nt;         // tiles in all, at least one
+};
+
+// The rows' chunk rc of sequence b; false: it has no rows.
+__device__ __forceinline__ bool item_of(const PromptArgs& a, int b, int rc, Item& m) {
+  m.q0 = min(max(__ldg(a.q_starts + b), 0), a.Tq);
+  const int n = min(max(__ldg(a.q_starts + b + 1), m.q0), a.Tq) - m.q0;
+  m.k0 = min(max(__ldg(a.k_starts + b), 0), a.Tk);
+  const int c = min(max(__ldg(a.k_starts + b + 1), m.k0), a.Tk) - m.k0;
+  m.first = c - n;
+  m.row0 = rc * kItemRows;
+  m.rows = min(min(n, a.max_q) * a.G - m.row0, kItemRows);
+  if (m.rows <= 0) return false;
+  const int last = m.first + (int)a.by_g.div(m.row0 + m.rows - 1);
+  m.hi = max(min(min(c, a.max_k), last + 1), 0);
+  m.lo = a.window > 0
+             ? min(max(m.first + (int)a.by_g.div(m.row0) - a.window + 1, 0), m.hi)
+             : 0;
+  m.tl = m.lo / kTile;
+  m.ts = a.window > 0 ? min((a.sinks + kTile - 1) / kTile, m.tl) : 0;
+  m.nt = max(m.ts + (m.hi + kTile - 1) / kTile - m.tl, 1);
+  return true;
+}
+
+// The first key of the item's tile t.
+__device__ __forceinline__ int key_of_tile(const Item& m, int t) {
+  return (t < m.ts ? t : m.tl + (t - m.ts)) * kTile;
+}
+
+// The list of work: for each sequence, row chunk and key head the item's
+// tiles.  It is cut into equal shares, one per CTA.
+struct Share {
+  int64_t s0, s1, total;
+  int b, rc, head, off;  // the item of unit s0, and the tile in it
+  int grid;              // CTAs with a share
+};
+
+// A segment of the share: an item's tiles [t0, t1).
+struct Seg {
+  Item m;
+  int head, t0, t1;
+  int whole;  // the item as a whole
+  int part;   // else the slot of its partial outputs
+  int more;   // segments follow
+};
+
+// This CTA's share, by the whole CTA.
+__device__ __forceinline__ void locate_share(const PromptArgs& a, Share& sh) {
+  __shared__ int64_t part[kThreads / 32];
+  __shared__ int count[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int64_t pairs = (int64_t)a.batch * a.rc_max;
+  const int64_t each = (pairs + kThreads - 1) / kThreads;
+  const int64_t p0 = min(tid * each, pairs), p1 = min(p0 + each, pairs);
+  const int b0 = (int)(p0 / a.rc_max), rc0 = (int)(p0 - (int64_t)b0 * a.rc_max);
+  int64_t own = 0;
+  int items = 0;
+  Item m;
+  for (int64_t p = p0, b = b0, rc = rc0; p < p1; ++p) {
+    if (item_of(a, (int)b, (int)rc, m)) {
+      own += m.nt;
+      ++items;
+    }
+    if (++rc == a.rc_max) {
+      rc = 0;
+      ++b;
+    }
+  }
+  own *= a.Hkv;
+  int64_t incl = own;
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t o = __shfl_up_sync(kFull, incl, d);
+    if (lane >= d) incl += o;
+  }
+  items = __reduce_add_sync(kFull, items);
+  if (lane == 31) {
+    part[warp] = incl;
+    count[warp] = items;
+  }
+  __syncthreads();
+  int64_t base = 0, total = 0, n = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) base += part[w];
+    total += part[w];
+    n += count[w];
+  }
+  // shares of at least four tiles, but every item may have a CTA of its own
+  const int64_t most = gridDim.x;
+  const int64_t grid = min(max(total / 4, min(n * a.Hkv, most)), most);
+  const int64_t s0 = blockIdx.x < grid ? total * blockIdx.x / grid : 0;
+  const int64_t s1 = blockIdx.x < grid ? total * (blockIdx.x + 1) / grid : 0;
+  const int64_t from = base + incl - own;
+  if (tid == 0) {
+    sh.s0 = s0;
+    sh.s1 = s1;
+    sh.total = total;
+    sh.grid = (int)grid;
+  }
+  if (s0 < s1 && from <= s0 && s0 < from + own) {
+    int64_t at = from;
+    for (int b = b0, rc = rc0;;) {
+      if (item_of(a, b, rc, m)) {
+        const int64_t u = (int64_t)m.nt * a.Hkv;
+        if (s0 < at + u) {
+          sh.b = b;
+          sh.rc = rc;
+          sh.head = (int)((s0 - at) / m.nt);
+          sh.off = (int)((s0 - at) % m.nt);
+          break;
+        }
+        at += u;
+      }
+      if (++rc == a.rc_max) {
+        rc = 0;
+        ++b;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// The CTA whose share holds unit x.
+__device__ __forceinline__ int cta_of(int64_t x, const Share& sh) {
+  return (int)(((x + 1) * sh.grid - 1) / sh.total);
+}
+
+// An operand whose rows run along K, 64 elements of M or N in each of 128 bytes,
+// 128-byte swizzled: 8-row groups 1024 bytes apart, 64-element blocks of M or N
+// `block` bytes apart.
+__device__ __forceinline__ uint64_t sw128_rows_desc(uint32_t addr, uint32_t block) {
+  uint64_t d = (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(block >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// kind::f16: A and B bf16 or fp16, A K-major, B K-major or (rows) along N; fp32
+// D, M = 128.
+__host__ __device__ constexpr uint32_t idesc16(int N, bool half, bool rows) {
+  return (1u << 4) | (half ? 0u : (1u << 7) | (1u << 10)) | (rows ? 1u << 16 : 0u) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kHalfRows >> 4) << 24);
+}
+
+// A box of 64 elements x 128 rows at (x, row, z), completing on `bar`.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int row,
+                                        int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(row), "r"(z)
+      : "memory");
+}
+
+// What a TMEM load has filled is not looked at before its wait.
+__device__ __forceinline__ void settle(float* s) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile(""
+                 : "+f"(s[i]), "+f"(s[i + 1]), "+f"(s[i + 2]), "+f"(s[i + 3]), "+f"(s[i + 4]),
+                   "+f"(s[i + 5]), "+f"(s[i + 6]), "+f"(s[i + 7]));
+}
+
+// Barriers.
+template <int D>
+struct Bars {
+  enum {
+    kFullAt = 0,                      // a tile of the ring is loaded
+    kEmpty = kFullAt + ring_of(D),    // and used
+    kClean = kEmpty + ring_of(D),     // a value tile holds nothing that is not seen
+    kSFull = kClean + kCleanRing,     // per half: its scores are in TMEM
+    kPFull = kSFull + 2,              // per half: its probabilities are, O rescaled
+    kODone = kPFull + 2,              // per half: the product with the values is done
+    kQFull = kODone + 2,              // per half: its queries are in shared memory
+    kQEmpty = kQFull + 2,             // per half: and used
+    kSegFull = kQEmpty + 2,           // a segment is described
+    kSegEmpty = kSegFull + kSegRing,  // and read by all
+    kCount = kSegEmpty + kSegRing
+  };
+  // The arrivals that complete a barrier's phase.
+  static __device__ __forceinline__ int arrivals(int i) {
+    if (i >= kSegEmpty) return kSegUsers;
+    if (i >= kPFull && i < kODone) return 4;
+    if (i >= kClean && i < kSFull) return 2;
+    return 1;
+  }
+};
+
+template <int D>
+struct Ctl {
+  uint64_t bars[Bars<D>::kCount];
+  Share share;
+  Seg segs[kSegRing];
+  uint32_t tmem;
+  uint32_t abort;
+};
+
+template <int D, bool kHalf>
+__global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_constant__ PromptArgs a) {
+  using B = Bars<D>;
+  constexpr int kBlocks = D / 64;               // 64-element column blocks of a row
+  constexpr uint32_t kBlock = kTile * 128;      // bytes of one, of 128 rows
+  constexpr int kRing = ring_of(D);
+  constexpr float kShift = kHalf ? 10.0f : 0.0f, kSlack = kHalf ? 4.0f : 8.0f;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Ctl<D> ctl;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sq = base, skv = base + q_bytes(D);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  volatile uint32_t* abort = &ctl.abort;
+  const auto bar = [&](int i) { return smem_addr(&ctl.bars[i]); };
+  const auto slot_at = [&](uint32_t u) { return skv + u % kRing * kv_bytes(D); };
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // joins as CTAs end
+  locate_share(a, ctl.share);
+  const Share& share = ctl.share;
+  if (share.s0 >= share.s1) {
+    if (tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < B::kCount; ++i) mbar_init(bar(i), B::arrivals(i));
+    fence_mbar_init();
+    ctl.abort = 0;
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&ctl.tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = __shfl_sync(kFull, ctl.tmem, 0);
+  const auto wait = [&](int i, uint32_t parity) {
+    return __all_sync(kFull, wait_bar(bar(i), parity, abort)) != 0;
+  };
+  uint32_t loaded = 0, skipped = 0xffffffffu;  // warp 1: tiles asked for, one withheld
+
+  if (warp >= kSoftWarp) {
+    // ------------------------------------------------------------- softmax
+    set_regs_up<kSoftRegs>();
+    const int half = (warp - kSoftWarp) / 4, rl = tid % kHalfRows;
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t ts = tmem + lanes + half * 128;
+    const uint32_t to = tmem + lanes + 256 + half * D;
+    // a factor of zero would make a masked score NaN
+    const float c = fmaxf(a.scale_log2, 0x1p-100f);
+    uint32_t n = 0;  // tiles of this half so far
+    bool ok = true;
+    for (uint32_t i = 0; ok; ++i) {
+      ok = wait(B::kSegFull + i % kSegRing, i / kSegRing & 1u);
+      if (!ok) break;
+      const Seg& seg = ctl.segs[i % kSegRing];
+      const Item& m = seg.m;
+      const int nt = seg.t1 - seg.t0, t0 = seg.t0, ts_tiles = m.ts, tl = m.tl;
+      const bool more = seg.more != 0;
+      if (half == 1 && m.rows <= kHalfRows) {  // no rows in this half
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B::kSegEmpty + i % kSegRing));
+        if (!more) break;
+        continue;
+      }
+      const bool whole = seg.whole != 0;
+      const int part = seg.part;
+      const int w0 = half * kHalfRows + warp % 4 * 32;  // the warp's first row
+      const int r = m.row0 + half * kHalfRows + rl;     // row of the sequence
+      const bool live = half * kHalfRows + rl < m.rows;
+      const int tok = (int)a.by_g.div(r);
+      const int64_t orow = (int64_t)(m.q0 + tok) * a.Hq + seg.head * a.G + (r - tok * a.G);
+      // the last key that the row sees, and for the warp's first and last row
+      const int pos = live ? min(m.first + tok, m.hi - 1) : -1;
+      const int pos_lo = min(m.first + (int)a.by_g.div(m.row0 + w0), m.hi - 1);
+      const int pos_hi = m.first + (int)a.by_g.div(m.row0 + min(w0 + 31, m.rows - 1));
+      const int lo_key = a.window > 0 ? m.first + tok - a.window + 1 : -(1 << 30);
+      const bool idle = w0 >= m.rows;  // no row: keep the barriers going
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B::kSegEmpty + i % kSegRing));
+      float M = -INFINITY, l = 0.0f;
+      for (int t = 0; t < nt; ++t, ++n) {
+        ok = wait(B::kSFull + half, n & 1u);
+        if (!ok) break;
+        fence_after();
+        if (!idle) {
+          const int kt = t0 + t;
+          const int kb = (kt < ts_tiles ? kt : tl + (kt - ts_tiles)) * kTile;
+          const bool full = kb + kTile <= pos_lo + 1 &&
+                            (a.window <= 0 || kb > pos_hi - a.window || kb + kTile <= a.sinks);
+          float s[kTile];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) tmem_ld32(ts + w * 32, s + w * 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int w = 0; w < 4; ++w) settle(s + w * 32);
+          if (__builtin_expect(!full, 0)) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int from = kb + w * 32;
+              const uint32_t on = sees(pos - from, lo_key - from, a.sinks - from);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(on >> e & 1u)) s[w * 32 + e] = -INFINITY;
+            }
+          }
+          const float x = c * fmaxf(fmaxf(top32(s), top32(s + 32)),
+                                    fmaxf(top32(s + 64), top32(s + 96)));
+          // ---- the sums' reference, moved seldom
+          const bool move = x > M + kSlack || (M == -INFINITY && x != -INFINITY);
+          if (__builtin_expect(__any_sync(kFull, move), 0)) {
+            const float al = move ? exp2_approx(M - x) : 1.0f;
+            if (move) M = x;
+            l *= al;
+            if (t > 0) {
+              ok = wait(B::kODone + half, (n - 1) & 1u);
+              if (!ok) break;
+              fence_after();
+              // few columns at a time: s stays in registers
+#pragma unroll 1
+              for (int d = 0; d < D; d += 16) {
+                float o[16];
+                tmem_ld16(to + d, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  asm volatile("" : "+f"(o[j]));
+                  o[j] *= al;
+                }
+                tmem_st16(to + d, reinterpret_cast<const uint32_t*>(o));
+              }
+            }
+          }
+          const float ref = or_zero(M) - kShift;
+          float b0 = 0.0f, b1 = 0.0f, b2 = 0.0f, b3 = 0.0f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float* v = s + w * 32;
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float y0, y1, y2, y3;
+              fma2s(y0, y1, v[e], v[e + 1], c, -ref);
+              fma2s(y2, y3, v[e + 2], v[e + 3], c, -ref);
+              y0 = exp2_approx(y0);
+              y1 = exp2_approx(y1);
+              y2 = exp2_approx(y2);
+              y3 = exp2_approx(y3);
+              sum2(b0, b1, b0, b1, y0, y1);
+              sum2(b2, b3, b2, b3, y2, y3);
+              p[e / 2] = pack16<kHalf>(y0, y1);
+              p[e / 2 + 1] = pack16<kHalf>(y2, y3);
+            }
+            tmem_st16(ts + w * 16, p);
+          }
+          l += (b0 + b1) + (b2 + b3);
+          tmem_wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B::kPFull + half));
+      }
+      // ---- the output row
+      if (ok) ok = wait(B::kODone + half, (n - 1) & 1u);
+      if (ok && !idle) {
+        fence_after();
+        const bool some = M != -INFINITY;
+        const float inv = some ? __frcp_rn(l) : 0.0f;
+        const float lse2 = some ? M - kShift + __log2f(l) : -INFINITY;
+        const int64_t prow = (int64_t)part * kItemRows + half * kHalfRows + rl;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          float o[32];
+          __syncwarp();
+          tmem_ld32(to + d, o);
+          tmem_wait_ld();
+          settle(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = some ? o[j] * inv : 0.0f;
+          if (!live) {
+          } else if (!whole) {
+            float4* dst = reinterpret_cast<float4*>(a.part_out + prow * D + d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              dst[j] = make_uint4(pack16<kHalf>(o[8 * j], o[8 * j + 1]),
+                                  pack16<kHalf>(o[8 * j + 2], o[8 * j + 3]),
+                                  pack16<kHalf>(o[8 * j + 4], o[8 * j + 5]),
+                                  pack16<kHalf>(o[8 * j + 6], o[8 * j + 7]));
+          }
+        }
+        if (live) {
+          if (!whole)
+            a.part_lse[prow] = lse2;
+          else if (a.lse)
+            a.lse[orow] = lse2 * kLn2;
+        }
+      }
+      if (!more) break;
+    }
+  } else {
+    set_regs_down<kOtherRegs>();
+  }
+  if (warp >= kSideWarp && warp < kSoftWarp) {
+    // ------------------------------------------- queries, unseen value rows
+    const int half = warp - kSideWarp;
+    constexpr int kRowLanes = D / 8, kPer = 32 / kRowLanes;
+    uint32_t n = 0, fills = 0;  // tiles, segments with rows in this half, so far
+    bool ok = true;
+    for (uint32_t i = 0; ok; ++i) {
+      ok = wait(B::kSegFull + i % kSegRing, i / kSegRing & 1u);
+      if (!ok) break;
+      const Seg seg = ctl.segs[i % kSegRing];
+      const Item& m = seg.m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B::kSegEmpty + i % kSegRing));
+      if (m.rows > half * kHalfRows) {
+        if (fills > 0) ok = wait(B::kQEmpty + half, (fills - 1) & 1u);
+        if (!ok) break;
+        ++fills;
+        const int ch = lane % kRowLanes;
+#pragma unroll 1
+        for (int g = 0; g < kHalfRows; g += 32) {  // rows g .. g + 31 of the half
+          const int rr = half * kHalfRows + g + lane, r = m.row0 + rr;
+          const int tok = (int)a.by_g.div(r);
+          const int64_t own = rr < m.rows ? (m.q0 + tok) * a.q_ts +
+                                                (int64_t)(seg.head * a.G + r - tok * a.G) * a.q_hs
+                                          : -1;
+          const int row = g + lane / kRowLanes;
+          const uint32_t dst = sq + half * kBlocks * kBlock + ch / 8 * kBlock + row * 128;
+#pragma unroll 4
+          for (int j = 0; j < kRowLanes; ++j) {
+            const int64_t off = __shfl_sync(kFull, own, j * kPer + lane / kRowLanes);
+            const uint32_t at = dst + j * kPer * 128 + ((ch ^ (row + j * kPer)) & 7) * 16;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at),
+                         "l"(a.q + (off < 0 ? 0 : off + ch * 8)), "r"(off < 0 ? 0 : 16)
+                         : "memory");
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B::kQFull + half));
+      }
+      for (int t = seg.t0; t < seg.t1 && ok; ++t, ++n) {
+        const uint32_t u = 2 * n + 1;
+        ok = wait(B::kFullAt + u % kRing, u / kRing & 1u);
+        if (!ok) break;
+        const int kb = key_of_tile(m, t);
+        // this warp's 64 rows of the tile
+        bool touched = false;
+#pragma unroll 1
+        for (int w = 2 * half; w < 2 * half + 2; ++w) {
+          const int from = kb + 32 * w;
+          const uint32_t on = sees(m.hi - 1 - from, m.lo - from, a.sinks - from);
+          if (on == kFull) continue;
+          touched = true;
+          const uint32_t at = slot_at(u) + (w * 32 + lane / 8) * 128 + lane % 8 * 16;
+#pragma unroll 1
+          for (int e = 0; e < 32; e += 4)
+            if (!(on >> (e + lane / 8) & 1u))
+#pragma unroll
+              for (int k = 0; k < kBlocks; ++k)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at + e * 128 +
+                                                                           k * kBlock),
+                             "r"(0)
+                             : "memory");
+        }
+        if (touched) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B::kClean + n % kCleanRing));
+      }
+      if (!seg.more) break;
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------- MMA issuer
+    constexpr uint32_t kQkDesc = idesc16(kTile, kHalf, false), kPvDesc = idesc16(D, kHalf, true);
+    // a descriptor's address field moves by (bytes >> 4)
+    const uint64_t dq = sw128_desc(sq), dk = sw128_desc(skv), dv = sw128_rows_desc(skv, D == 128 ? kBlock : 1024);
+    const uint32_t elected = elect_one();
+    const auto issue_s = [&](int half, uint32_t u) {
+      const uint64_t qa = dq + half * (kBlocks * kBlock >> 4);
+      const uint64_t kb = dk + u % kRing * (kv_bytes(D) >> 4);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(elected, tmem + half * 128, qa + (k / 4 * (kBlock >> 4) + k % 4 * 2),
+               kb + (k / 4 * (kBlock >> 4) + k % 4 * 2), kQkDesc, k > 0);
+      mma_commit(elected, bar(B::kSFull + half));
+    };
+    const auto issue_o = [&](int half, uint32_t u, bool first) {
+      const uint64_t vb = dv + u % kRing * (kv_bytes(D) >> 4);
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_ts(elected, tmem + 256 + half * D, tmem + half * 128 + k * 8, vb + k * (2048 >> 4),
+               kPvDesc, !first || k > 0);
+      mma_commit(elected, bar(B::kODone + half));
+    };
+    bool ok = true;
+    uint32_t n = 0, n_a = 0, n_b = 0;  // tiles so far: of the CTA, of each half
+    uint32_t q_a = 0, q_b = 0;         // segments so far, of each half
+    for (uint32_t i = 0; ok; ++i) {
+      ok = wait(B::kSegFull + i % kSegRing, i / kSegRing & 1u);
+      if (!ok) break;
+      const Seg& seg = ctl.segs[i % kSegRing];
+      const int nt = seg.t1 - seg.t0;
+      const int halves = seg.m.rows > kHalfRows ? 2 : 1;
+      const bool more = seg.more != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B::kSegEmpty + i % kSegRing));
+      uint32_t u = 2 * n;
+      ok = wait(B::kFullAt + u % kRing, u / kRing & 1u);
+      for (int h = 0; h < halves && ok; ++h) {
+        ok = wait(B::kQFull + h, (h ? q_b : q_a) & 1u);
+        if (!ok) break;
+        fence_after();
+        issue_s(h, u);
+        if (nt == 1 && more) mma_commit(elected, bar(B::kQEmpty + h));
+      }
+      ++q_a;
+      q_b += halves - 1;
+      if (ok && (nt > 1 || more)) mma_commit(elected, bar(B::kEmpty + u % kRing));
+      for (int t = 0; t < nt && ok; ++t, ++n) {
+        const uint32_t uv = 2 * n + 1, uk = 2 * n + 2;
+        const bool last = t + 1 == nt;
+        ok = wait(B::kFullAt + uv % kRing, uv / kRing & 1u) &&
+             wait(B::kClean + n % kCleanRing, n / kCleanRing & 1u);
+        for (int h = 0; h < halves && ok; ++h) {
+          ok = wait(B::kPFull + h, (h ? n_b : n_a) & 1u);
+          if (!ok) break;
+          fence_after();
+          issue_o(h, uv, t == 0);
+          if (!last) {
+            if (h == 0) ok = wait(B::kFullAt + uk % kRing, uk / kRing & 1u);
+            if (!ok) break;
+            issue_s(h, uk);
+            if (t + 2 == nt && more) mma_commit(elected, bar(B::kQEmpty + h));
+          }
+        }
+        if (!ok) break;
+        ++n_a;
+        n_b += halves - 1;
+        // (nothing waits for the last tile of all)
+        if (!last || more) mma_commit(elected, bar(B::kEmpty + uv % kRing));
+        if (!last) mma_commit(elected, bar(B::kEmpty + uk % kRing));
+      }
+      if (!more) break;
+    }
+  } else if (warp == kLoadWarp) {
+    // -------------------------------------------------- work list and tiles
+    int b = share.b, rc = share.rc, head = share.head, t0 = share.off;
+    int64_t at = share.s0;
+    int4 cut = make_int4(0, 0, 0, 0);
+    // (testing hook, see fp4idx_test_withhold_next: a tile that is not loaded)
+    const uint32_t held = blockIdx.x == 0 && a.withhold >= 0 ? 2u * a.withhold : 0xffffffffu;
+    bool ok = true;
+    for (uint32_t i = 0; at < share.s1 && ok; ++i) {
+      if (i >= kSegRing) ok = wait(B::kSegEmpty + i % kSegRing, (i / kSegRing + 1) & 1u);
+      if (!ok) break;
+      Seg sg;
+      item_of(a, b, rc, sg.m);
+      sg.head = head;
+      sg.t0 = t0;
+      sg.t1 = (int)min((int64_t)sg.m.nt, t0 + (share.s1 - at));
+      sg.whole = t0 == 0 && sg.t1 == sg.m.nt;
+      sg.part = 2 * blockIdx.x + (t0 == 0 && i > 0 ? 1 : 0);
+      if (!sg.whole && t0 == 0)  // the first fragment of a cut item
+        cut = make_int4(b, rc, head,
+                        (cta_of(at + sg.m.nt - 1, share) - (int)blockIdx.x + 1) * 2 +
+                            (sg.part & 1));
+      at += sg.t1 - t0;
+      sg.more = at < share.s1;
+      if (lane == 0) {
+        ctl.segs[i % kSegRing] = sg;
+        mbar_arrive(bar(B::kSegFull + i % kSegRing));
+      }
+      for (int t = sg.t0; t < sg.t1 && ok; ++t) {
+        const int row = sg.m.k0 + key_of_tile(sg.m, t);
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t u = loaded;
+          if (u >= (uint32_t)kRing) ok = wait(B::kEmpty + u % kRing, (u / kRing + 1) & 1u);
+          if (!ok) break;
+          ++loaded;
+          if (u == held) {
+            skipped = u;
+            continue;
+          }
+          if (lane == 0) {
+            const uint32_t full = bar(B::kFullAt + u % kRing);
+            mbar_arrive_expect_tx(full, kv_bytes(D));
+            const CUtensorMap* map = kv ? &a.vmap : &a.kmap;
+            const int x = head * (kv ? a.vx : a.kx), z = head * (kv ? a.vz : a.kz);
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k)
+              tma_box(slot_at(u) + k * kBlock, map, x + k * 64, row, z, full);
+          }
+          __syncwarp();
+        }
+      }
+      t0 = 0;
+      if (++head == a.Hkv && sg.more) {
+        head = 0;
+        Item it;
+        do {
+          if (++rc == a.rc_max) {
+            rc = 0;
+            ++b;
+          }
+        } while (!item_of(a, b, rc, it));
+      }
+    }
+    if (lane == 0) a.cuts[blockIdx.x] = cut;
+  }
+
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (*abort) {
+    // Copies and MMAs in flight land before shared memory and TMEM are
+    // released.  A commit stands for its own lane's MMAs: the lane that was
+    // elected to issue them.
+    if (warp == kLoadWarp)
+      for (uint32_t u = loaded > (uint32_t)kRing ? loaded - kRing : 0; u < loaded; ++u)
+        if (u != skipped) mbar_wait_bounded(bar(B::kFullAt + u % kRing), u / kRing & 1u);
+    if (warp == kMmaWarp && elect_one()) {
+      flag_error(a.err, FP4IDX_ERRFLAG_TIMEOUT);
+      const uint32_t b = bar(B::kQFull);  // re-used: one arrival by the commit
+      asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(b) : "memory");
+      mbar_init(b, 1);
+      fence_mbar_init();
+      mma_commit(1, b);
+      mbar_wait_bounded(b, 0);
+    }
+    __syncthreads();
+  }
+  __syncwarp();
+  if (warp == kMmaWarp) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+// Joins the partial outputs of the items that a share's end cut (join_rows).
+// Blocks (CTA whose share begins the item, 32 of its rows), four rows a warp.
+template <int D, bool kHalf>
+__global__ __launch_bounds__(256) void join_prompt_kernel(const __grid_constant__ PromptArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kBlocks = kItemRows / 32;
+  const int cta = blockIdx.x / kBlocks;
+  const int4 cut = a.cuts[cta];
+  const int n = cut.w / 2;
+  if (n < 2) return;
+  Item m;
+  item_of(a, cut.x, cut.y, m);
+  const int lane = threadIdx.x % 32;
+  const auto slot = [&](int f) { return (int64_t)2 * (cta + f) + (f == 0 ? cut.w & 1 : 0); };
+  constexpr int kV = D / 32, kRows = 4;
+  const int r0 = blockIdx.x % kBlocks * 32 + threadIdx.x / 32 * kRows;
+  if (r0 >= m.rows) return;
+  float top[kRows], den[kRows], o[kRows][kV];
+  join_rows<D, kRows, kItemRows>(a.part_out, a.part_lse, n, r0, m.rows, lane, slot, top, den, o);
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if (r0 + k >= m.rows) continue;
+    const int r = m.row0 + r0 + k, tok = (int)a.by_g.div(r);
+    const bool some = top[k] != -INFINITY;
+    const float inv = some ? __frcp_rn(den[k]) : 0.0f;
+    const int64_t orow = (int64_t)(m.q0 + tok) * a.Hq + cut.z * a.G + (r - tok * a.G);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * kV);
+#pragma unroll
+    for (int j = 0; j < kV; j += 2)
+      dst[j / 2] = pack16<kHalf>(o[k][j] * inv, o[k][j + 1] * inv);
+    if (a.lse && lane == 0)
+      a.lse[orow] = some ? (top[k] + __log2f(den[k])) * kLn2 : -INFINITY;
+  }
+}
+
+template <int D, bool kHalf>
+fp4idx_status launch_prompt(const PromptArgs& a, int grid, cudaStream_t stream) {
+  static SmemOnce once;
+  if (!once.set(prompt_kernel<D, kHalf>, smem_bytes(D))) return FP4IDX_ERR_CUDA;
+  if (launch_kernel(prompt_kernel<D, kHalf>, (unsigned)grid, kThreads, smem_bytes(D), stream, a) !=
+      cudaSuccess)
+    return FP4IDX_ERR_CUDA;
+  return launch_after(join_prompt_kernel<D, kHalf>, (unsigned)(grid * (kItemRows / 32)), 256,
+                      stream, a) == cudaSuccess
+             ? FP4IDX_OK
+             : FP4IDX_ERR_CUDA;
+}
+
+struct Workspace {
+  int64_t part_lse, cuts, total;  // offsets in bytes; partial outputs at 0
+};
+
+// Two partial outputs per CTA (an item cut at its share's start and one at
+// its end), and the cut items.
+Workspace workspace_of(int64_t head_dim) {
+  Workspace w;
+  w.part_lse = 2 * kMaxGrid * kItemRows * head_dim * 4;
+  w.cuts = w.part_lse + 2 * kMaxGrid * kItemRows * 4;
+  w.total = w.cuts + (kMaxGrid * 16 + 255) / 256 * 256;
+  return w;
+}
+
+bool workspace_args_ok(int64_t batch, int64_t max_q, int64_t num_heads, int64_t kv_heads,
+                       int64_t head_dim) {
+  return batch >= 0 && max_q >= 1 && kv_heads >= 1 && kv_heads <= 65535 &&
+         num_heads >= kv_heads && num_heads % kv_heads == 0 &&
+         (head_dim == 64 || head_dim == 128) && batch < (1ll << 31) && num_heads < (1ll << 20) &&
+         max_q < (1ll << 31) / num_heads;
+}
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's call that describes a tensor to the TMA unit.
+EncodeTiled encode_tiled() {
+  static std::atomic<EncodeTiled> found{nullptr};
+  EncodeTiled f = found.load(std::memory_order_acquire);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult got;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                       &got) != cudaSuccess ||
+      got != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeTiled>(p);
+  found.store(f, std::memory_order_release);
+  return f;
+}
+
+// How the rows of k or v lie: a token's heads within its stride (the map's first
+// axis spans them), or a head's tokens within its stride (its last axis).
+struct Rows {
+  uint64_t dim[3], stride[2];  // strides of the second and third axis, in bytes
+  int32_t x, z;                // a head's step in the first and last coordinate
+  bool shape_ok, align_ok;
+};
+
+Rows rows_of(int64_t tokens, int64_t heads, int64_t head_dim, int64_t ts, int64_t hs) {
+  Rows r = {};
+  if (heads == 1) hs = 0;
+  if (tokens == 1) ts = (heads - 1) * hs + head_dim;
+  if (ts < 0 || hs < 0 || ts >= (1ll << 38) || hs >= (1ll << 38)) return r;
+  const int64_t span = (heads - 1) * hs + head_dim;
+  r.align_ok = ts % 8 == 0 && hs % 8 == 0;
+  if (ts >= span) {
+    r.shape_ok = span < (1ll << 31) && ts <= (1ll << 38) / (tokens > 0 ? tokens : 1);
+    r.dim[0] = span;
+    r.dim[1] = tokens;
+    r.dim[2] = 1;
+    r.stride[0] = ts * 2;
+    r.stride[1] = r.shape_ok ? ts * 2 * tokens : 0;
+    r.x = (int32_t)hs;
+  } else if (ts >= head_dim && hs >= ts && (tokens - 1) <= (hs - head_dim) / ts) {
+    r.shape_ok = hs % ts == 0 && hs <= (1ll << 38) / heads;
+    r.dim[0] = head_dim;
+    r.dim[1] = tokens;
+    r.dim[2] = heads;
+    r.stride[0] = ts * 2;
+    r.stride[1] = hs * 2;
+    r.z = 1;
+  }
+  return r;
+}
+
+bool encode(CUtensorMap* map, const void* base, const Rows& r, bool half) {
+  const EncodeTiled f = encode_tiled();
+  if (!f) return false;
+  const cuuint64_t dim[3] = {r.dim[0], r.dim[1], r.dim[2]}, stride[2] = {r.stride[0], r.stride[1]};
+  const cuuint32_t box[3] = {64, kTile, 1}, step[3] = {1, 1, 1};
+  return f(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+           const_cast<void*>(base), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Testing hook: the tile that the next launch withholds (-1: none), taken once.
+std::atomic<int64_t> g_prompt_withhold{-1};
+
+}  // namespace
+
+void prompt_withhold_next(int64_t index) { g_prompt_withhold.store(index); }
+
+}  // namespace fp4idx_impl
+
+using namespace fp4idx_impl;
+
+extern "C" size_t fp4idx_prompt_workspace_bytes(int64_t batch, int64_t max_q, int64_t num_heads,
+                                                int64_t kv_heads, int64_t head_dim) {
+  if (!workspace_args_ok(batch, max_q, num_heads, kv_heads, head_dim)) return 0;
+  return (size_t)workspace_of(head_dim).total;
+}
+
+extern "C" fp4idx_status fp4idx_prompt_attention(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+    int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+    int64_t v_head_stride, int dtype, const int32_t* q_starts, const int32_t* k_starts,
+    int64_t max_q, int64_t max_k, int64_t window, int64_t sinks, float softmax_scale, void* out,
+    float* lse, int64_t batch, int64_t q_tokens, int64_t k_tokens, int64_t num_heads,
+    int64_t kv_heads, int64_t head_dim, void* workspace, size_t workspace_bytes,
+    uint32_t* err_flags, void* stream) {
+  if (batch < 0 || q_tokens < 0 || k_tokens < 0) return FP4IDX_ERR_SHAPE;
+  if (batch == 0 || q_tokens == 0) return FP4IDX_OK;
+  if (!q || !q_starts || !out || !workspace || (k_tokens > 0 && (!k || !v)))
+    return FP4IDX_ERR_NULL;
+  if (!workspace_args_ok(batch, max_q, num_heads, kv_heads, head_dim) || max_k < 0 ||
+      q_tokens >= (1ll << 31) / num_heads || k_tokens >= (1 << 30) || max_q >= (1 << 30) ||
+      max_k >= (1 << 30))
+    return FP4IDX_ERR_SHAPE;
+  const Rows kr = rows_of(k_tokens, kv_heads, head_dim, k_token_stride, k_head_stride);
+  const Rows vr = rows_of(k_tokens, kv_heads, head_dim, v_token_stride, v_head_stride);
+  if (k_tokens > 0 && (!kr.shape_ok || !vr.shape_ok)) return FP4IDX_ERR_SHAPE;
+  const Workspace w = workspace_of(head_dim);
+  if (workspace_bytes < (size_t)w.total) return FP4IDX_ERR_SCRATCH;
+  if (!dtype_ok(dtype) || !isfinite(softmax_scale) || softmax_scale < 0.0f || window < 0 ||
+      sinks < 0)
+    return FP4IDX_ERR_ARG;
+  if (!aligned(q, 16) || q_token_stride % 8 || q_head_stride % 8 || !aligned(k, 16) ||
+      !aligned(v, 16) || (k_tokens > 0 && (!kr.align_ok || !vr.align_ok)) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(workspace, 16) || !aligned(q_starts, 4) ||
+      !aligned(k_starts, 4) || !aligned(err_flags, 4))
+    return FP4IDX_ERR_ALIGN;
+  PromptArgs a = {};
+  const bool half = dtype == FP4IDX_FP16;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.q_starts = q_starts;
+  a.k_starts = k_starts ? k_starts : q_starts;
+  a.max_q = (int32_t)max_q;
+  a.max_k = (int32_t)max_k;
+  // a window that holds every key is no window
+  a.window = window < max_k ? (int32_t)window : 0;
+  a.sinks = (int32_t)(sinks < max_k ? sinks : max_k);
+  a.batch = (int32_t)batch;
+  a.Tq = (int32_t)q_tokens;
+  a.Tk = (int32_t)k_tokens;
+  a.Hq = (int32_t)num_heads;
+  a.Hkv = (int32_t)kv_heads;
+  a.G = (int32_t)(num_heads / kv_heads);
+  a.by_g = make_fastdiv((uint32_t)a.G);
+  const int64_t most_q = max_q < q_tokens ? max_q : q_tokens;
+  a.rc_max = (int32_t)((most_q * a.G + kItemRows - 1) / kItemRows);
+  a.withhold = -1;
+  a.scale_log2 = softmax_scale * kLog2e;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  a.part_out = reinterpret_cast<float*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  a.cuts = reinterpret_cast<int4*>(ws + w.cuts);
+  a.err = err_flags;
+  if (k_tokens > 0) {
+    a.kx = kr.x;
+    a.kz = kr.z;
+    a.vx = vr.x;
+    a.vz = vr.z;
+    if (!encode(&a.kmap, k, kr, half) || !encode(&a.vmap, v, vr, half)) return FP4IDX_ERR_CUDA;
+  } else {  // no key: one row of the workspace, which no query sees
+    const Rows none = rows_of(1, 1, head_dim, head_dim, head_dim);
+    if (!encode(&a.kmap, workspace, none, half)) return FP4IDX_ERR_CUDA;
+    a.vmap = a.kmap;
+  }
+  if (g_prompt_withhold.load(std::memory_order_relaxed) >= 0) {
+    const int64_t held = g_prompt_withhold.exchange(-1);
+    if (held < (1 << 28)) a.withhold = (int32_t)held;
+  }
+  // (at most 2^31 items of at most 2^23 tiles)
+  const int64_t items = ((q_tokens * a.G + kItemRows - 1) / kItemRows + batch) * kv_heads;
+  const int64_t units = items * (max_k / kTile + 1);
+  const int grid = units < kMaxGrid ? (int)units : kMaxGrid;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (head_dim == 128)
+    return half ? launch_prompt<128, true>(a, grid, s) : launch_prompt<128, false>(a, grid, s);
+  return half ? launch_prompt<64, true>(a, grid, s) : launch_prompt<64, false>(a, grid, s);
+}

@@ -5,8 +5,9 @@ missing: there is no CPU path.  Build it with
 ``python -m fp4_sparse_attention_fp4idx_gb300.build``.
 
 Two layers:
-  * ``lib()`` -- the raw C ABI (names and argument order of include/fp4idx.h
-    and include/fp4idx_attention.h, plain integers for pointers).
+  * ``lib()`` -- the raw C ABI (names and argument order of include/fp4idx.h,
+    include/fp4idx_attention.h and include/fp4idx_step.h, plain integers for
+    pointers).
   * torch wrappers with the same names (minus the ``fp4idx_`` prefix) that
     check dtypes/devices, allocate outputs with torch, pass ``data_ptr()``s
     and the current CUDA stream (or ``stream=``, on which outputs that are not
@@ -21,11 +22,13 @@ import functools
 import os
 import re
 import threading
+from typing import Any, NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfp4idx.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp4idx.h")
 ATTENTION_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp4idx_attention.h")
+STEP_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp4idx_step.h")
 
 ROPE_NEOX = 0
 ROPE_INTERLEAVED = 1
@@ -35,6 +38,7 @@ ERRFLAG_POSITION = 0x1
 ERRFLAG_SLOT = 0x2
 ERRFLAG_TIMEOUT = 0x4
 ERRFLAG_PAGE = 0x8
+ERRFLAG_FULL = 0x10
 
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_ARG, ERR_CUDA, ERR_SCRATCH = range(7)
 STATIC_STAGING_BYTES = 64 << 20  # FP4IDX_STATIC_STAGING_BYTES
@@ -93,6 +97,17 @@ _SIGS = {
         _INT, [_P, _I64, _I64, _INT, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _F, _P, _P, _I64,
                _I64, _I64, _P, ctypes.c_size_t, _P, _P]),
     "fp4idx_topk_tokens": (_INT, [_P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P]),
+    "fp4idx_batch_extend": (
+        _INT, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _P, _P]),
+    "fp4idx_pages_release": (
+        _INT, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P]),
+    "fp4idx_rope_qk": (
+        _INT, [_P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _INT,
+               _I64, _P, _I64, _P, _INT, _INT, _P, _P, _I64, _I64, _INT, _I64, _P, _P]),
+    "fp4idx_prompt_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64]),
+    "fp4idx_prompt_attention": (
+        _INT, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _INT, _P, _P, _I64, _I64, _I64,
+               _I64, _F, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, ctypes.c_size_t, _P, _P]),
     "fp4idx_default_weight_scale": (_F, [_I64]),
     "fp4idx_test_withhold_next": (_INT, [_INT, _I64]),
     "fp4idx_status_string": (ctypes.c_char_p, [_INT]),
@@ -167,12 +182,15 @@ def rope_style_code(style) -> int:
 TEST_PREPASS = 0
 TEST_SCORER = 1
 TEST_ATTENTION = 2
+TEST_PROMPT = 3
 
 
 def test_withhold_next(kernel: int, index: int) -> None:
     """Testing hook: the next launch of `kernel` (TEST_PREPASS: the streaming
     pre-pass; TEST_SCORER: the scorers; TEST_ATTENTION: attention over the
-    8-bit cache) leaves out the copies of work item `index` of its first CTA, so its bounded waits run out (TIMEOUT flag)."""
+    8-bit cache; TEST_PROMPT: attention of prompts) leaves out the copies of
+    work item `index` of its first CTA, so its bounded waits run out (TIMEOUT
+    flag)."""
     _check(_lib.fp4idx_test_withhold_next(int(kernel), int(index)), "fp4idx_test_withhold_next")
 
 
@@ -1075,3 +1093,232 @@ def topk_tokens(logits, k: int, *, row_lens=None, indices=None, counts=None, str
           logits.stride(0) if R > 1 else N, lens, indices.data_ptr(),
           indices.stride(0) if R > 1 else k, counts.data_ptr(), R, N, k)
     return indices, counts
+
+
+# ------------------------------------ pages and maps, rotary positions, prompts
+class BatchMaps(NamedTuple):
+    """What batch_extend writes for the step's other calls."""
+    q_starts: Any      # int32 [batch+1]
+    context_lens: Any  # int32 [batch]
+    slot_mapping: Any  # int64 [num_tokens]
+    positions: Any     # int64 [num_tokens]
+    seq_ids: Any       # int32 [num_tokens]
+    row_lens: Any      # int32 [num_tokens]
+
+
+def _pool(first, second, names, block_table, free_pages, free_count):
+    """Checks of two vectors of lengths and the page pool; (device index, batch,
+    the pool's C arguments)."""
+    torch = _torch()
+    i32 = torch.int32
+    dev = block_table.get_device() if isinstance(block_table, torch.Tensor) else -1
+    _fits(block_table, i32, 2, dev, "block_table")
+    _fits(first, i32, 1, dev, names[0])
+    _fits(second, i32, 1, dev, names[1])
+    _fits(free_pages, i32, 1, dev, "free_pages")
+    _fits(free_count, i32, 1, dev, "free_count")
+    batch, pages = block_table.shape
+    _dense(first, (batch,), names[0])
+    _dense(second, (batch,), names[1])
+    _dense(free_pages, free_pages.shape, "free_pages")
+    if free_count.shape[0] != 1:
+        raise ValueError("free_count must be [1]")
+    st = block_table.stride()
+    if pages > 1 and st[1] != 1:
+        raise ValueError("block_table must have unit column stride")
+    if batch > 1 and st[0] < pages:
+        raise ValueError("block_table's rows must not overlap")
+    return dev, batch, (block_table.data_ptr(), st[0] if batch > 1 else pages, pages,
+                        free_pages.data_ptr(), free_count.data_ptr(), free_pages.shape[0])
+
+
+def batch_extend(cached_lens, new_lens, block_table, free_pages, free_count, num_tokens: int, *,
+                 q_starts=None, context_lens=None, slot_mapping=None, positions=None, seq_ids=None,
+                 row_lens=None, err_flags=None, stream=None) -> BatchMaps:
+    """The next tokens of a batch: new_lens int32 [batch] tokens behind
+    cached_lens int32 [batch] ones.  Takes the pages that they need off the
+    stack free_pages int32 [n] / free_count int32 [1] into block_table int32
+    [batch, pages], in place, and returns the maps of the step's num_tokens tokens
+    (slot -1, position 0, sequence 0, row length 0 behind the last one).  A
+    sequence that cannot be served keeps its pages and length, its tokens get slot
+    -1, and ERRFLAG_FULL is raised.  context_lens is the next step's cached_lens."""
+    torch = _torch()
+    dev, batch, pool = _pool(cached_lens, new_lens, ("cached_lens", "new_lens"), block_table,
+                             free_pages, free_count)
+    if num_tokens < 0:
+        raise ValueError("num_tokens must not be negative")
+    given = (q_starts, context_lens, slot_mapping, positions, seq_ids, row_lens)
+    i32, i64 = torch.int32, torch.int64
+    maps = []
+    with _on(stream):
+        for t, n, dt, name in zip(given, (batch + 1, batch, *[num_tokens] * 4),
+                                  (i32, i32, i64, i64, i32, i32), BatchMaps._fields):
+            if t is None:
+                t = torch.empty(n, dtype=dt, device=block_table.device)
+            else:
+                _fits(t, dt, 1, dev, name)
+                _dense(t, (n,), name)
+            maps.append(t)
+    _call(_lib.fp4idx_batch_extend, dev, stream, cached_lens.data_ptr(), new_lens.data_ptr(),
+          *pool, *(t.data_ptr() for t in maps), batch, num_tokens, _flags(err_flags, dev))
+    return BatchMaps(*maps)
+
+
+def pages_release(held_lens, kept_lens, block_table, free_pages, free_count, *, err_flags=None,
+                  stream=None) -> None:
+    """Gives pages back to the stack, in place: of the pages that held_lens int32
+    [batch] tokens fill, those behind the first kept_lens int32 [batch] tokens (0:
+    the sequence has ended).  Their entries of block_table become -1.  Undoes a
+    batch_extend that went before it."""
+    dev, batch, pool = _pool(held_lens, kept_lens, ("held_lens", "kept_lens"), block_table,
+                             free_pages, free_count)
+    _call(_lib.fp4idx_pages_release, dev, stream, held_lens.data_ptr(), kept_lens.data_ptr(),
+          *pool, batch, _flags(err_flags, dev))
+
+
+AXES_SECTIONS = 0
+AXES_INTERLEAVED = 1
+
+
+@functools.lru_cache(maxsize=64)
+def _sections(sections):
+    return (ctypes.c_int32 * len(sections))(*sections)
+
+
+def rope_qk(q, k, positions, cos, sin, *, rope_style="neox", sections=None,
+            interleaved_axes: bool = False, q_out=None, k_out=None, err_flags=None, stream=None):
+    """Rotary positions of queries and keys -> (q_out, k_out).  q, k bf16 or fp16
+    [T, heads, D] (strides multiples of 8; k may be None), cos, sin fp32 [max_pos,
+    R/2]: the first R elements of a row are turned, the others copied.  positions
+    int64 [T], or [axes, T] with `sections`, the pairs that each axis turns: ranges
+    of pairs, or dealt in turn (interleaved_axes).  q_out may be q and k_out k (in
+    place); outputs that are not given are allocated dense."""
+    torch = _torch()
+    dt = _type16(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads, D]")
+    dev = q.get_device()
+    T, Hq, D = q.shape
+    qs = _rows16(q, Hq, D, dev, "q")
+    Hk, ks = 0, (0, 0)
+    if k is not None:
+        if _type16(k, "k") != dt:
+            raise TypeError("q and k must have the same dtype")
+        if k.dim() != 3 or k.shape[0] != T:
+            raise ValueError("k must be [T, heads, D] with q's tokens")
+        Hk = k.shape[1]
+        ks = _rows16(k, Hk, D, dev, "k")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _fits(cos, torch.float32, 2, dev, "cos")
+    _fits(sin, torch.float32, 2, dev, "sin")
+    _dense(cos, cos.shape, "cos")
+    _dense(sin, cos.shape, "sin")
+    max_pos, half = cos.shape
+    axes = 1
+    if isinstance(positions, torch.Tensor) and positions.dim() == 2:
+        axes = positions.shape[0]
+        if sections is None and axes > 1:
+            raise ValueError("positions of several axes need sections")
+    _fits(positions, torch.int64, positions.dim() if axes > 1 or (
+        isinstance(positions, torch.Tensor) and positions.dim() == 2) else 1, dev, "positions")
+    if positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
+        raise ValueError("positions must be [T] or [axes, T] with unit token stride")
+    sections = (half,) if sections is None else tuple(int(n) for n in sections)
+    if len(sections) != axes:
+        raise ValueError("sections must have an entry for each axis of positions")
+    with _on(stream):
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        if k_out is None and k is not None:
+            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device)
+    _fits(q_out, q.dtype, 3, dev, "q_out")
+    qo, ko = _rows16(q_out, Hq, D, dev, "q_out"), (0, 0)
+    if q_out.shape[0] != T:
+        raise ValueError("q_out must have q's shape")
+    if k is not None:
+        _fits(k_out, q.dtype, 3, dev, "k_out")
+        ko = _rows16(k_out, Hk, D, dev, "k_out")
+        if k_out.shape[0] != T:
+            raise ValueError("k_out must have k's shape")
+    _call(_lib.fp4idx_rope_qk, dev, stream, q.data_ptr(), *qs, q_out.data_ptr(), *qo, Hq,
+          k.data_ptr() if Hk else None, *ks, k_out.data_ptr() if Hk else None, *ko, Hk, dt, D,
+          positions.data_ptr(), positions.stride(0) if axes > 1 else T, _sections(sections), axes,
+          AXES_INTERLEAVED if interleaved_axes else AXES_SECTIONS, cos.data_ptr(), sin.data_ptr(),
+          max_pos, 2 * half, rope_style_code(rope_style), T, _flags(err_flags, dev))
+    return q_out, k_out
+
+
+def prompt_workspace_bytes(batch: int, max_q: int, num_heads: int, kv_heads: int,
+                           head_dim: int) -> int:
+    """Workspace of prompt_attention; 0 for arguments out of range."""
+    return _lib.fp4idx_prompt_workspace_bytes(batch, max_q, num_heads, kv_heads, head_dim)
+
+
+@functools.lru_cache(maxsize=256)
+def _prompt_workspace(batch, max_q, num_heads, kv_heads, head_dim):
+    return prompt_workspace_bytes(batch, max_q, num_heads, kv_heads, head_dim) or 16
+
+
+def prompt_attention(q, k, v, q_starts, max_q: int, *, k_starts=None, max_k=None, window: int = 0,
+                     sinks: int = 0, softmax_scale=None, out=None, lse=None, workspace=None,
+                     err_flags=None, stream=None):
+    """Causal attention of packed sequences over their own keys and values ->
+    (out [Tq, H, D] of q's dtype, lse fp32 [Tq, H]).  q bf16 or fp16 [Tq, H, D], k,
+    v [Tk, kv_heads, D] (strides multiples of 8); q_starts int32 [batch+1], max_q
+    the longest.  Whole prompts, or, with k_starts int32 [batch+1] and max_k,
+    queries that end a longer run of keys: chunks and single tokens.  window > 0: a
+    query sees the last `window` keys and the first `sinks`.  softmax_scale defaults
+    to D^-1/2.  Rows of out and lse in no sequence are left as they were."""
+    torch = _torch()
+    dt = _type16(q, "q")
+    if _type16(k, "k") != dt or _type16(v, "v") != dt:
+        raise TypeError("q, k and v must have the same dtype")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [Tq, H, D], k and v [Tk, kv_heads, D]")
+    dev = q.get_device()
+    (Tq, H, D), (Tk, Hk, _) = q.shape, k.shape
+    qs, ks, vs = _rows16(q, H, D, dev, "q"), _rows16(k, Hk, D, dev, "k"), \
+        _rows16(v, Hk, D, dev, "v")
+    if v.shape[0] != Tk:
+        raise ValueError("k and v must have the same tokens")
+    if Hk == 0 or H % Hk:
+        raise ValueError("q's heads must be a multiple of k's")
+    _fits(q_starts, torch.int32, 1, dev, "q_starts")
+    batch = q_starts.shape[0] - 1
+    if batch < 0 or not q_starts.is_contiguous():
+        raise ValueError("q_starts must be contiguous [batch+1]")
+    kst = None
+    if k_starts is not None:
+        _fits(k_starts, torch.int32, 1, dev, "k_starts")
+        _dense(k_starts, (batch + 1,), "k_starts")
+        if max_k is None:
+            raise ValueError("k_starts needs max_k, the longest run of keys")
+        kst = k_starts.data_ptr()
+    elif Tk != Tq:
+        raise ValueError("without k_starts, q and k must have the same tokens")
+    if max_k is None:
+        max_k = max_q
+    with _on(stream):
+        if out is None:
+            out = torch.empty((Tq, H, D), dtype=q.dtype, device=q.device)
+        else:
+            _fits(out, q.dtype, 3, dev, "out")
+            _dense(out, (Tq, H, D), "out")
+        if lse is None:
+            lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
+        else:
+            _fits(lse, torch.float32, 2, dev, "lse")
+            _dense(lse, (Tq, H), "lse")
+        if workspace is None:
+            workspace = torch.empty(_prompt_workspace(batch, max_q, H, Hk, D), dtype=torch.uint8,
+                                    device=q.device)
+        else:
+            _fits(workspace, torch.uint8, 1, dev, "workspace")
+            _dense(workspace, workspace.shape, "workspace")
+    _call(_lib.fp4idx_prompt_attention, dev, stream, q.data_ptr(), *qs, k.data_ptr(), *ks,
+          v.data_ptr(), *vs, dt, q_starts.data_ptr(), kst, max_q, max_k, window, sinks,
+          D ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), lse.data_ptr(),
+          batch, Tq, Tk, H, Hk, D, workspace.data_ptr(), workspace.numel(),
+          _flags(err_flags, dev))
+    return out, lse

@@ -497,14 +497,16 @@ float fp4idx_default_weight_scale(int64_t num_heads);
  * scorers (FP4IDX_TEST_SCORER; tiles count in that CTA's order, and a tile's
  * partner in its stage pair is left out with it), or of the attention kernels
  * (FP4IDX_TEST_ATTENTION) a 128-key tile of the one for many rows, or a stage
- * of the rings of the one for few.  The waits for it then run out after their
+ * of the rings of the one for few, or the keys of a 128-key tile of attention of
+ * prompts (FP4IDX_TEST_PROMPT).  The waits for it then run out after their
  * 1 s limit: that launch raises FP4IDX_ERRFLAG_TIMEOUT, leaves part of its
  * outputs unwritten or wrong, drains its copies in flight and returns; later
  * launches are unaffected.  The hook is taken by that one launch (an index past
  * the CTA's work withholds nothing).  Returns FP4IDX_ERR_ARG for an unknown
  * kernel or a negative index.
  */
-enum { FP4IDX_TEST_PREPASS = 0, FP4IDX_TEST_SCORER = 1, FP4IDX_TEST_ATTENTION = 2 };
+enum { FP4IDX_TEST_PREPASS = 0, FP4IDX_TEST_SCORER = 1, FP4IDX_TEST_ATTENTION = 2,
+       FP4IDX_TEST_PROMPT = 3 };
 fp4idx_status fp4idx_test_withhold_next(int kernel, int64_t index);
 
 /* Static, NUL-terminated description of a status code. */
