@@ -552,8 +552,10 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(bar(B::kQFull + half));
       }
       for (int t = seg.t0; t < seg.t1 && ok; ++t, ++n) {
-        const uint32_t u = 2 * n + 1;
-        ok = wait(B::kFullAt + u % kRing, u / kRing & 1u);
+        // (the keys' phase too: a wait that skips one takes the next for it)
+        const uint32_t uk = 2 * n, u = uk + 1;
+        ok = wait(B::kFullAt + uk % kRing, uk / kRing & 1u) &&
+             wait(B::kFullAt + u % kRing, u / kRing & 1u);
         if (!ok) break;
         const int kb = key_of_tile(m, t);
         // this warp's 64 rows of the tile
