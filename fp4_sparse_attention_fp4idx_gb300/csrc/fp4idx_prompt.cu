@@ -265,6 +265,23 @@ __device__ __forceinline__ void settle(float* s) {
                    "+f"(s[i + 5]), "+f"(s[i + 6]), "+f"(s[i + 7]));
 }
 
+// The wait of a whole warp behind a first look that failed.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  return __all_sync(kFull, wait_bar(bar, parity, abort)) != 0;
+}
+
+// A place in the ring of tiles and the phase of its barriers.
+template <int kRing>
+struct Place {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kRing) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 // Barriers.
 template <int D>
 struct Bars {
@@ -274,7 +291,7 @@ struct Bars {
     kClean = kEmpty + ring_of(D),     // a value tile holds nothing that is not seen
     kSFull = kClean + kCleanRing,     // per half: its scores are in TMEM
     kPFull = kSFull + 2,              // per half: its probabilities are, O rescaled
-    kODone = kPFull + 2,              // per half: the product with the values is done
+    kODone = kPFull + 2,              // per half: a segment's last product is done
     kQFull = kODone + 2,              // per half: its queries are in shared memory
     kQEmpty = kQFull + 2,             // per half: and used
     kSegFull = kQEmpty + 2,           // a segment is described
@@ -339,8 +356,12 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
   __syncthreads();
   fence_after();
   const uint32_t tmem = __shfl_sync(kFull, ctl.tmem, 0);
+  const uint32_t bars = bar(0);
+  // (a first look without a loop: its code costs a hundred cycles on the issuer's
+  // path from one half's softmax to its products)
   const auto wait = [&](int i, uint32_t parity) {
-    return __all_sync(kFull, wait_bar(bar(i), parity, abort)) != 0;
+    const uint32_t b = bars + i * 8;
+    return __all_sync(kFull, mbar_try_wait(b, parity)) || wait_on(b, parity, abort);
   };
   uint32_t loaded = 0, skipped = 0xffffffffu;  // warp 1: tiles asked for, one withheld
 
@@ -353,7 +374,8 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
     const uint32_t to = tmem + lanes + 256 + half * D;
     // a factor of zero would make a masked score NaN
     const float c = fmaxf(a.scale_log2, 0x1p-100f);
-    uint32_t n = 0;  // tiles of this half so far
+    uint32_t n = 0, all = 0;  // tiles so far: of this half, of the CTA
+    uint32_t done = 0;        // segments of this half so far
     bool ok = true;
     for (uint32_t i = 0; ok; ++i) {
       ok = wait(B::kSegFull + i % kSegRing, i / kSegRing & 1u);
@@ -362,7 +384,9 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
       const Item& m = seg.m;
       const int nt = seg.t1 - seg.t0, t0 = seg.t0, ts_tiles = m.ts, tl = m.tl;
       const bool more = seg.more != 0;
-      if (half == 1 && m.rows <= kHalfRows) {  // no rows in this half
+      const bool both = m.rows > kHalfRows;
+      if (half == 1 && !both) {  // no rows in this half
+        all += nt;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B::kSegEmpty + i % kSegRing));
         if (!more) break;
@@ -381,18 +405,26 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
       const int pos_hi = m.first + (int)a.by_g.div(m.row0 + min(w0 + 31, m.rows - 1));
       const int lo_key = a.window > 0 ? m.first + tok - a.window + 1 : -(1 << 30);
       const bool idle = w0 >= m.rows;  // no row: keep the barriers going
+      // one thread says when tiles and queries are used: what the tensor core has
+      // been asked for before scores that are there is done
+      const bool says = lane == 0 && warp % 4 == 0, says_all = says && half == (both ? 1 : 0);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B::kSegEmpty + i % kSegRing));
       float M = -INFINITY, l = 0.0f;
-      for (int t = 0; t < nt; ++t, ++n) {
+      for (int t = 0; t < nt; ++t, ++n, ++all) {
+        const int kt = t0 + t;
+        const int kb = (kt < ts_tiles ? kt : tl + (kt - ts_tiles)) * kTile;
+        const bool full = kb + kTile <= pos_lo + 1 &&
+                          (a.window <= 0 || kb > pos_hi - a.window || kb + kTile <= a.sinks);
         ok = wait(B::kSFull + half, n & 1u);
         if (!ok) break;
         fence_after();
+        if (says_all) {
+          if (t > 0) mbar_arrive(bar(B::kEmpty + (2 * all - 1) % kRing));
+          mbar_arrive(bar(B::kEmpty + 2 * all % kRing));
+        }
+        if (says && t + 1 == nt) mbar_arrive(bar(B::kQEmpty + half));
         if (!idle) {
-          const int kt = t0 + t;
-          const int kb = (kt < ts_tiles ? kt : tl + (kt - ts_tiles)) * kTile;
-          const bool full = kb + kTile <= pos_lo + 1 &&
-                            (a.window <= 0 || kb > pos_hi - a.window || kb + kTile <= a.sinks);
           float s[kTile];
 #pragma unroll
           for (int w = 0; w < 4; ++w) tmem_ld32(ts + w * 32, s + w * 32);
@@ -418,9 +450,6 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
             if (move) M = x;
             l *= al;
             if (t > 0) {
-              ok = wait(B::kODone + half, (n - 1) & 1u);
-              if (!ok) break;
-              fence_after();
               // few columns at a time: s stays in registers
 #pragma unroll 1
               for (int d = 0; d < D; d += 16) {
@@ -466,7 +495,8 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(bar(B::kPFull + half));
       }
       // ---- the output row
-      if (ok) ok = wait(B::kODone + half, (n - 1) & 1u);
+      if (ok) ok = wait(B::kODone + half, done++ & 1u);
+      if (says_all) mbar_arrive(bar(B::kEmpty + (2 * all - 1) % kRing));
       if (ok && !idle) {
         fence_after();
         const bool some = M != -INFINITY;
@@ -589,26 +619,26 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
     // a descriptor's address field moves by (bytes >> 4)
     const uint64_t dq = sw128_desc(sq), dk = sw128_desc(skv), dv = sw128_rows_desc(skv, D == 128 ? kBlock : 1024);
     const uint32_t elected = elect_one();
-    const auto issue_s = [&](int half, uint32_t u) {
+    const auto issue_s = [&](int half, uint32_t slot) {
       const uint64_t qa = dq + half * (kBlocks * kBlock >> 4);
-      const uint64_t kb = dk + u % kRing * (kv_bytes(D) >> 4);
+      const uint64_t kb = dk + slot * (kv_bytes(D) >> 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         mma_ss(elected, tmem + half * 128, qa + (k / 4 * (kBlock >> 4) + k % 4 * 2),
                kb + (k / 4 * (kBlock >> 4) + k % 4 * 2), kQkDesc, k > 0);
       mma_commit(elected, bar(B::kSFull + half));
     };
-    const auto issue_o = [&](int half, uint32_t u, bool first) {
-      const uint64_t vb = dv + u % kRing * (kv_bytes(D) >> 4);
+    const auto issue_o = [&](int half, uint32_t slot, bool first) {
+      const uint64_t vb = dv + slot * (kv_bytes(D) >> 4);
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
         mma_ts(elected, tmem + 256 + half * D, tmem + half * 128 + k * 8, vb + k * (2048 >> 4),
                kPvDesc, !first || k > 0);
-      mma_commit(elected, bar(B::kODone + half));
     };
     bool ok = true;
-    uint32_t n = 0, n_a = 0, n_b = 0;  // tiles so far: of the CTA, of each half
-    uint32_t q_a = 0, q_b = 0;         // segments so far, of each half
+    uint32_t n = 0, n_b = 0;    // tiles so far: of the CTA (and half A), of half B
+    uint32_t q_a = 0, q_b = 0;  // segments so far, of each half
+    Place<kRing> at;            // the next tile
     for (uint32_t i = 0; ok; ++i) {
       ok = wait(B::kSegFull + i % kSegRing, i / kSegRing & 1u);
       if (!ok) break;
@@ -618,41 +648,36 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
       const bool more = seg.more != 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B::kSegEmpty + i % kSegRing));
-      uint32_t u = 2 * n;
-      ok = wait(B::kFullAt + u % kRing, u / kRing & 1u);
+      ok = wait(B::kFullAt + at.slot, at.phase);
       for (int h = 0; h < halves && ok; ++h) {
         ok = wait(B::kQFull + h, (h ? q_b : q_a) & 1u);
         if (!ok) break;
         fence_after();
-        issue_s(h, u);
-        if (nt == 1 && more) mma_commit(elected, bar(B::kQEmpty + h));
+        issue_s(h, at.slot);
       }
       ++q_a;
       q_b += halves - 1;
-      if (ok && (nt > 1 || more)) mma_commit(elected, bar(B::kEmpty + u % kRing));
+      at.next();
       for (int t = 0; t < nt && ok; ++t, ++n) {
-        const uint32_t uv = 2 * n + 1, uk = 2 * n + 2;
+        const uint32_t v = at.slot;  // keys' and values' tiles take turns
         const bool last = t + 1 == nt;
-        ok = wait(B::kFullAt + uv % kRing, uv / kRing & 1u) &&
-             wait(B::kClean + n % kCleanRing, n / kCleanRing & 1u);
+        at.next();
+        // (a clean tile has been loaded)
+        ok = wait(B::kClean + n % kCleanRing, n / kCleanRing & 1u) &&
+             (last || wait(B::kFullAt + at.slot, at.phase));
         for (int h = 0; h < halves && ok; ++h) {
-          ok = wait(B::kPFull + h, (h ? n_b : n_a) & 1u);
+          ok = wait(B::kPFull + h, (h ? n_b : n) & 1u);
           if (!ok) break;
           fence_after();
-          issue_o(h, uv, t == 0);
-          if (!last) {
-            if (h == 0) ok = wait(B::kFullAt + uk % kRing, uk / kRing & 1u);
-            if (!ok) break;
-            issue_s(h, uk);
-            if (t + 2 == nt && more) mma_commit(elected, bar(B::kQEmpty + h));
-          }
+          issue_o(h, v, t == 0);
+          if (last)
+            mma_commit(elected, bar(B::kODone + h));
+          else
+            issue_s(h, at.slot);
         }
         if (!ok) break;
-        ++n_a;
         n_b += halves - 1;
-        // (nothing waits for the last tile of all)
-        if (!last || more) mma_commit(elected, bar(B::kEmpty + uv % kRing));
-        if (!last) mma_commit(elected, bar(B::kEmpty + uk % kRing));
+        if (!last) at.next();
       }
       if (!more) break;
     }
