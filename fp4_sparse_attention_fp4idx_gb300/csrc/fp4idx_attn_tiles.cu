@@ -876,7 +876,10 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(const AttnArgs a) {
   const int r0 = blockIdx.x % kBlocks * 32 + threadIdx.x / 32 * kRows;
   if (r0 >= m.rows) return;
   float top[kRows], den[kRows], o[kRows][kV];
-  join_rows<D, kRows, kItemRows>(a.part_out, a.part_lse, n, r0, m.rows, lane, slot, top, den, o);
+  const auto at = [&](int64_t place, int row) {
+    return (place * kItemRows + row) * D + lane * kV;
+  };
+  join_rows<D, kRows, kItemRows>(a.part_out, a.part_lse, n, r0, m.rows, slot, at, top, den, o);
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     const int r = m.row0 + r0 + k;

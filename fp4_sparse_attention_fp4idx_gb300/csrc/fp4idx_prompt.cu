@@ -72,10 +72,11 @@ __host__ __device__ constexpr uint32_t smem_bytes(int D) {
 }
 
 struct PromptArgs {
-  CUtensorMap kmap, vmap;
+  CUtensorMap kmap, vmap, qmap;
   int32_t kx, kz, vx, vz;  // a head's step in the maps' first and last coordinate
   const uint16_t* q;
   int64_t q_ts, q_hs;
+  int32_t q_tma;  // queries are loaded by TMA: whole tokens fill a half
   const int32_t* q_starts;
   const int32_t* k_starts;
   int32_t max_q, max_k, window, sinks;
@@ -86,7 +87,7 @@ struct PromptArgs {
   float scale_log2;
   uint16_t* out;
   float* lse;
-  float* part_out;  // [slot][kItemRows][D] normalised partial outputs
+  float* part_out;  // normalised partial outputs, by part_at
   float* part_lse;  // [slot][kItemRows], log2
   // [grid]: the item that begins in a CTA's share and ends in another's:
   // sequence, row chunk, key head, CTAs * 2 + the first one's slot (0: none)
@@ -135,6 +136,14 @@ __device__ __forceinline__ int key_of_tile(const Item& m, int t) {
 // 128); shares of equal tiles left the CTA with the shortest items 1.5 times the
 // others' time.
 constexpr int kStart = 3;
+
+// Where element d (a multiple of 4, and up to 3 more) of an item's row lies in
+// partial output `place`: the rows of four elements together, so that a warp
+// writes 512 bytes on end.
+template <int D>
+__device__ __forceinline__ int64_t part_at(int64_t place, int d, int row) {
+  return ((place * (D / 4) + d / 4) * kItemRows + row) * 4 + d % 4;
+}
 
 // The list of work: for each sequence, row chunk and key head kStart units and
 // the item's tiles, a unit each.  It is cut into equal shares, one per CTA.
@@ -303,11 +312,12 @@ struct Bars {
     kQEmpty = kQFull + 2,             // per half: and used
     kSegFull = kQEmpty + 2,           // a segment is described
     kSegEmpty = kSegFull + kSegRing,  // and read by all
-    kCount = kSegEmpty + kSegRing
+    kEnd = kSegEmpty + kSegRing,      // everything in flight is done
+    kCount
   };
   // The arrivals that complete a barrier's phase.
   static __device__ __forceinline__ int arrivals(int i) {
-    if (i >= kSegEmpty) return kSegUsers;
+    if (i >= kSegEmpty && i < kEnd) return kSegUsers;
     if (i >= kPFull && i < kODone) return 4;
     if (i >= kClean && i < kSFull) return 2;
     return 1;
@@ -372,6 +382,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
     return __all_sync(kFull, mbar_try_wait(b, parity)) || wait_on(b, parity, abort);
   };
   uint32_t loaded = 0, skipped = 0xffffffffu;  // warp 1: tiles asked for, one withheld
+  uint32_t fills = 0;  // warps 2, 3: times that queries were asked for
 
   if (warp >= kSoftWarp) {
     // ------------------------------------------------------------- softmax
@@ -510,7 +521,12 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
         const bool some = M != -INFINITY;
         const float inv = some ? __frcp_rn(l) : 0.0f;
         const float lse2 = some ? M - kShift + __log2f(l) : -INFINITY;
-        const int64_t prow = (int64_t)part * kItemRows + half * kHalfRows + rl;
+        // four lanes turn their rows' 64 bytes into four times 64 bytes of a row: a
+        // store then touches 8 rows, not 32
+        int64_t to_row[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to_row[j] = __shfl_sync(kFull, orow, (lane & ~3) + j);
+        const uint32_t lives = __ballot_sync(kFull, live) >> (lane & ~3);
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           float o[32];
@@ -520,22 +536,37 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
           settle(o);
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = some ? o[j] * inv : 0.0f;
-          if (!live) {
-          } else if (!whole) {
-            float4* dst = reinterpret_cast<float4*>(a.part_out + prow * D + d);
+          if (!whole) {
+            if (live)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<float4*>(a.part_out +
+                                           part_at<D>(part, d + j, half * kHalfRows + rl)) =
+                    make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + d);
+            uint32_t u[4][4];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[j / 4][j % 4] = pack16<kHalf>(o[2 * j], o[2 * j + 1]);
+#pragma unroll
+            for (int x = 1; x < 4; x *= 2)  // lanes x apart change places
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (!(j & x))
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const bool up = (lane & x) != 0;
+                    const uint32_t got = __shfl_xor_sync(kFull, up ? u[j][e] : u[j + x][e], x);
+                    u[j][e] = up ? got : u[j][e];
+                    u[j + x][e] = up ? u[j + x][e] : got;
+                  }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              dst[j] = make_uint4(pack16<kHalf>(o[8 * j], o[8 * j + 1]),
-                                  pack16<kHalf>(o[8 * j + 2], o[8 * j + 3]),
-                                  pack16<kHalf>(o[8 * j + 4], o[8 * j + 5]),
-                                  pack16<kHalf>(o[8 * j + 6], o[8 * j + 7]));
+              if (lives >> j & 1u)
+                *reinterpret_cast<uint4*>(a.out + to_row[j] * D + d + lane % 4 * 8) =
+                    make_uint4(u[j][0], u[j][1], u[j][2], u[j][3]);
           }
         }
+        const int64_t prow = (int64_t)part * kItemRows + half * kHalfRows + rl;
         if (live) {
           if (!whole)
             a.part_lse[prow] = lse2;
@@ -551,8 +582,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
   if (warp >= kSideWarp && warp < kSoftWarp) {
     // ------------------------------------------- queries, unseen value rows
     const int half = warp - kSideWarp;
-    constexpr int kRowLanes = D / 8, kPer = 32 / kRowLanes;
-    uint32_t n = 0, fills = 0;  // tiles, segments with rows in this half, so far
+    uint32_t n = 0;  // tiles so far
     bool ok = true;
     for (uint32_t i = 0; ok; ++i) {
       ok = wait(B::kSegFull + i % kSegRing, i / kSegRing & 1u);
@@ -565,29 +595,36 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
         if (fills > 0) ok = wait(B::kQEmpty + half, (fills - 1) & 1u);
         if (!ok) break;
         ++fills;
-        const int ch = lane % kRowLanes;
-#pragma unroll 1
-        for (int g = 0; g < kHalfRows; g += 32) {  // rows g .. g + 31 of the half
-          const int rr = half * kHalfRows + g + lane, r = m.row0 + rr;
-          const int tok = (int)a.by_g.div(r);
-          const int64_t own = rr < m.rows ? (m.q0 + tok) * a.q_ts +
-                                                (int64_t)(seg.head * a.G + r - tok * a.G) * a.q_hs
-                                          : -1;
-          const int row = g + lane / kRowLanes;
-          const uint32_t dst = sq + half * kBlocks * kBlock + ch / 8 * kBlock + row * 128;
-#pragma unroll 4
-          for (int j = 0; j < kRowLanes; ++j) {
-            const int64_t off = __shfl_sync(kFull, own, j * kPer + lane / kRowLanes);
-            const uint32_t at = dst + j * kPer * 128 + ((ch ^ (row + j * kPer)) & 7) * 16;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at),
-                         "l"(a.q + (off < 0 ? 0 : off + ch * 8)), "r"(off < 0 ? 0 : 16)
-                         : "memory");
+        const uint32_t to = sq + half * kBlocks * kBlock;
+        if (a.q_tma) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(B::kQFull + half), kHalfRows * D * 2);
+            const int tok = m.q0 + (int)a.by_g.div(m.row0 + half * kHalfRows);
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k)
+              tma_box(to + k * kBlock, &a.qmap, k * 64, seg.head * a.G, tok, bar(B::kQFull + half));
           }
+        } else {
+#pragma unroll 1
+          for (int row = lane; row < kHalfRows; row += 32) {  // a row a lane
+            const int rr = half * kHalfRows + row, r = m.row0 + rr;
+            const int tok = (int)a.by_g.div(r);
+            const bool real = rr < m.rows;
+            const uint16_t* src = a.q;
+            if (real)
+              src += (m.q0 + tok) * a.q_ts + (int64_t)(seg.head * a.G + r - tok * a.G) * a.q_hs;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                               to + c / 8 * kBlock + row * 128 + ((c ^ row) & 7) * 16),
+                           "l"(src + c * 8), "r"(real ? 16 : 0)
+                           : "memory");
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B::kQFull + half));
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B::kQFull + half));
       }
       for (int t = seg.t0; t < seg.t1 && ok; ++t, ++n) {
         // (the keys' phase too: a wait that skips one takes the next for it)
@@ -769,12 +806,11 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
     if (warp == kLoadWarp)
       for (uint32_t u = loaded > (uint32_t)kRing ? loaded - kRing : 0; u < loaded; ++u)
         if (u != skipped) mbar_wait_bounded(bar(B::kFullAt + u % kRing), u / kRing & 1u);
+    if (a.q_tma && warp >= kSideWarp && warp < kSoftWarp && fills > 0)
+      mbar_wait_bounded(bar(B::kQFull + warp - kSideWarp), (fills - 1) & 1u);
     if (warp == kMmaWarp && elect_one()) {
       flag_error(a.err, FP4IDX_ERRFLAG_TIMEOUT);
-      const uint32_t b = bar(B::kQFull);  // re-used: one arrival by the commit
-      asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(b) : "memory");
-      mbar_init(b, 1);
-      fence_mbar_init();
+      const uint32_t b = bar(B::kEnd);
       mma_commit(1, b);
       mbar_wait_bounded(b, 0);
     }
@@ -807,7 +843,8 @@ __global__ __launch_bounds__(256) void join_prompt_kernel(const __grid_constant_
   const int r0 = blockIdx.x % kBlocks * 32 + threadIdx.x / 32 * kRows;
   if (r0 >= m.rows) return;
   float top[kRows], den[kRows], o[kRows][kV];
-  join_rows<D, kRows, kItemRows>(a.part_out, a.part_lse, n, r0, m.rows, lane, slot, top, den, o);
+  const auto at = [&](int64_t place, int row) { return part_at<D>(place, lane * kV, row); };
+  join_rows<D, kRows, kItemRows>(a.part_out, a.part_lse, n, r0, m.rows, slot, at, top, den, o);
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     if (r0 + k >= m.rows) continue;
@@ -912,11 +949,30 @@ Rows rows_of(int64_t tokens, int64_t heads, int64_t head_dim, int64_t ts, int64_
   return r;
 }
 
-bool encode(CUtensorMap* map, const void* base, const Rows& r, bool half) {
+// The same of q, heads before tokens, if a half's rows are whole tokens and a
+// token's heads lie within its stride.
+bool query_rows(Rows& r, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t ts,
+                int64_t hs) {
+  if (kHalfRows % group) return false;
+  if (heads == 1) hs = head_dim;
+  if (tokens == 1) ts = heads * hs;
+  if (hs < head_dim || ts < heads * hs || ts % hs || ts > (1ll << 38) / tokens) return false;
+  r = {};
+  r.dim[0] = head_dim;
+  r.dim[1] = heads;
+  r.dim[2] = tokens;
+  r.stride[0] = hs * 2;
+  r.stride[1] = ts * 2;
+  return true;
+}
+
+// A map of boxes of 64 elements x box1 x box2.
+bool encode(CUtensorMap* map, const void* base, const Rows& r, bool half, uint32_t box1 = kTile,
+            uint32_t box2 = 1) {
   const EncodeTiled f = encode_tiled();
   if (!f) return false;
   const cuuint64_t dim[3] = {r.dim[0], r.dim[1], r.dim[2]}, stride[2] = {r.stride[0], r.stride[1]};
-  const cuuint32_t box[3] = {64, kTile, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, box1, box2}, step[3] = {1, 1, 1};
   return f(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
            const_cast<void*>(base), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1010,6 +1066,9 @@ extern "C" fp4idx_status fp4idx_prompt_attention(
     if (!encode(&a.kmap, workspace, none, half)) return FP4IDX_ERR_CUDA;
     a.vmap = a.kmap;
   }
+  Rows qr;
+  a.q_tma = query_rows(qr, q_tokens, num_heads, a.G, head_dim, q_token_stride, q_head_stride);
+  if (a.q_tma && !encode(&a.qmap, q, qr, half, a.G, kHalfRows / a.G)) return FP4IDX_ERR_CUDA;
   if (g_prompt_withhold.load(std::memory_order_relaxed) >= 0) {
     const int64_t held = g_prompt_withhold.exchange(-1);
     if (held < (1 << 28)) a.withhold = (int32_t)held;
