@@ -298,6 +298,35 @@ struct Place {
   }
 };
 
+// 64 scores of a row -> their probabilities 2^(c s - ref), written to TMEM in the
+// elements' type; the unrounded ones are added to `sum`.
+template <bool kHalf>
+__device__ __forceinline__ void probabilities(const float* s, float c, float ref, uint32_t to,
+                                              float& sum) {
+  float b0 = sum, b1 = 0.0f, b2 = 0.0f, b3 = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float* v = s + w * 32;
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      float y0, y1, y2, y3;
+      fma2s(y0, y1, v[e], v[e + 1], c, -ref);
+      fma2s(y2, y3, v[e + 2], v[e + 3], c, -ref);
+      y0 = exp2_approx(y0);
+      y1 = exp2_approx(y1);
+      y2 = exp2_approx(y2);
+      y3 = exp2_approx(y3);
+      sum2(b0, b1, b0, b1, y0, y1);
+      sum2(b2, b3, b2, b3, y2, y3);
+      p[e / 2] = pack16<kHalf>(y0, y1);
+      p[e / 2 + 1] = pack16<kHalf>(y2, y3);
+    }
+    tmem_st16(to + w * 16, p);
+  }
+  sum = (b0 + b1) + (b2 + b3);
+}
+
 // Barriers.
 template <int D>
 struct Bars {
@@ -306,7 +335,8 @@ struct Bars {
     kEmpty = kFullAt + ring_of(D),    // and used
     kClean = kEmpty + ring_of(D),     // a value tile holds nothing that is not seen
     kSFull = kClean + kCleanRing,     // per half: its scores are in TMEM
-    kPFull = kSFull + 2,              // per half: its probabilities are, O rescaled
+    kPHalf = kSFull + 2,              // per half: 64 keys' probabilities are, O rescaled
+    kPFull = kPHalf + 2,              // per half: and the others'
     kODone = kPFull + 2,              // per half: a segment's last product is done
     kQFull = kODone + 2,              // per half: its queries are in shared memory
     kQEmpty = kQFull + 2,             // per half: and used
@@ -318,7 +348,7 @@ struct Bars {
   // The arrivals that complete a barrier's phase.
   static __device__ __forceinline__ int arrivals(int i) {
     if (i >= kSegEmpty && i < kEnd) return kSegUsers;
-    if (i >= kPFull && i < kODone) return 4;
+    if (i >= kPHalf && i < kODone) return 4;
     if (i >= kClean && i < kSFull) return 2;
     return 1;
   }
@@ -460,8 +490,10 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
                 if (!(on >> e & 1u)) s[w * 32 + e] = -INFINITY;
             }
           }
-          const float x = c * fmaxf(fmaxf(top32(s), top32(s + 32)),
-                                    fmaxf(top32(s + 64), top32(s + 96)));
+          const auto top = [&]() {
+            return c * fmaxf(fmaxf(top32(s), top32(s + 32)), fmaxf(top32(s + 64), top32(s + 96)));
+          };
+          const float x = top();
           // ---- the sums' reference, moved seldom
           const bool move = x > M + kSlack || (M == -INFINITY && x != -INFINITY);
           if (__builtin_expect(__any_sync(kFull, move), 0)) {
@@ -484,30 +516,17 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
               }
             }
           }
-          const float ref = or_zero(M) - kShift;
-          float b0 = 0.0f, b1 = 0.0f, b2 = 0.0f, b3 = 0.0f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float* v = s + w * 32;
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float y0, y1, y2, y3;
-              fma2s(y0, y1, v[e], v[e + 1], c, -ref);
-              fma2s(y2, y3, v[e + 2], v[e + 3], c, -ref);
-              y0 = exp2_approx(y0);
-              y1 = exp2_approx(y1);
-              y2 = exp2_approx(y2);
-              y3 = exp2_approx(y3);
-              sum2(b0, b1, b0, b1, y0, y1);
-              sum2(b2, b3, b2, b3, y2, y3);
-              p[e / 2] = pack16<kHalf>(y0, y1);
-              p[e / 2 + 1] = pack16<kHalf>(y2, y3);
-            }
-            tmem_st16(ts + w * 16, p);
-          }
-          l += (b0 + b1) + (b2 + b3);
+          float sum = 0.0f;
+          probabilities<kHalf>(s, c, or_zero(M) - kShift, ts, sum);
           tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B::kPHalf + half));
+          probabilities<kHalf>(s + 64, c, or_zero(M) - kShift, ts + 32, sum);
+          l += sum;
+          tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(bar(B::kPHalf + half));
         }
         fence_before();
         __syncwarp();
@@ -673,12 +692,13 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
                kb + (k / 4 * (kBlock >> 4) + k % 4 * 2), kQkDesc, k > 0);
       mma_commit(elected, bar(B::kSFull + half));
     };
-    const auto issue_o = [&](int half, uint32_t slot, bool first) {
+    // the product with 64 keys' values
+    const auto issue_o = [&](int half, uint32_t slot, int keys, bool first) {
       const uint64_t vb = dv + slot * (kv_bytes(D) >> 4);
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_ts(elected, tmem + 256 + half * D, tmem + half * 128 + k * 8, vb + k * (2048 >> 4),
-               kPvDesc, !first || k > 0);
+      for (int k = 0; k < 4; ++k)
+        mma_ts(elected, tmem + 256 + half * D, tmem + half * 128 + keys / 2 + k * 8,
+               vb + (keys / 16 + k) * (2048 >> 4), kPvDesc, !first || k > 0);
     };
     bool ok = true;
     uint32_t n = 0, n_b = 0;    // tiles so far: of the CTA (and half A), of half B
@@ -711,10 +731,15 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
         ok = wait(B::kClean + n % kCleanRing, n / kCleanRing & 1u) &&
              (last || wait(B::kFullAt + at.slot, at.phase));
         for (int h = 0; h < halves && ok; ++h) {
-          ok = wait(B::kPFull + h, (h ? n_b : n) & 1u);
+          const uint32_t parity = (h ? n_b : n) & 1u;
+          ok = wait(B::kPHalf + h, parity);
           if (!ok) break;
           fence_after();
-          issue_o(h, v, t == 0);
+          issue_o(h, v, 0, t == 0);
+          ok = wait(B::kPFull + h, parity);
+          if (!ok) break;
+          fence_after();
+          issue_o(h, v, 64, false);
           if (last)
             mma_commit(elected, bar(B::kODone + h));
           else
