@@ -4,11 +4,13 @@
 // What bounds it.  Each element is read and written once, 4 bytes, against three
 // operations: HBM.  The cosines and sines of a token are shared by its heads.
 //
-// Layout.  A unit is 8 pairs of a row, two 16-byte words.  A warp takes a token
-// and a range of its heads, queries' before keys'; a lane keeps its 8 cosines
-// and sines in registers over the heads where a row's units divide a warp (they
-// are loaded again for each head, from L1, where not).  Which axis turns a pair
-// is two bits of a table made on the host.
+// Layout.  A unit is 8 pairs of a row, two 16-byte words; what is not turned is
+// copied by units of two words more.  A thread keeps the cosines and sines of one
+// unit of a token in registers and turns that unit in every `groups`-th head,
+// queries' before keys', kUnroll of them in flight; its first rows are asked for
+// before the angles, whose addresses wait for the positions.  Consecutive threads
+// take a head's units, then the next head's, so that a warp reads a run of memory.
+// Which axis turns a pair is two bits of a table made on the host.
 
 #include "fp4idx_attn.cuh"
 #include "fp4idx_step.h"
@@ -16,9 +18,9 @@
 namespace fp4idx_impl {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256;
 constexpr int kMaxPairs = 512;
-constexpr int kUnroll = 4;  // units of a lane in flight
+constexpr int kUnroll = 4;  // heads of a thread in flight
 
 struct RopeSide {
   const uint16_t* in;
@@ -36,10 +38,10 @@ struct RopeArgs {
   const float* sin;
   int64_t max_pos;
   int32_t half;      // pairs of a row
-  int32_t units;     // half / 8
+  int32_t units;     // of a row: half / 8 that are turned, the others copied
+  int32_t groups;    // threads that share a token's unit
+  FastDiv by_units, by_groups;
   int32_t tail;      // 16-byte words of a row that are copied
-  int32_t per_warp;  // heads of a warp
-  int32_t splits;    // warps of a token
   int64_t T;
   uint32_t* err;
   uint32_t axis_bits[kMaxPairs / 16];  // pair i: bits 2 (i % 16) of word i / 16
@@ -52,122 +54,107 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = x;
 }
 
-template <bool kHalf, bool kNeox, bool kFixed>
-__global__ __launch_bounds__(kThreads) void rope_kernel(const __grid_constant__ RopeArgs a) {
-  const int lane = threadIdx.x % 32;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-  const int64_t t = w / a.splits;
+template <bool kHalf, bool kNeox>
+__global__ __launch_bounds__(kThreads, 3) void rope_kernel(const __grid_constant__ RopeArgs a) {
+  const uint32_t id = blockIdx.x * kThreads + threadIdx.x;  // unit u, group g, token t
+  const uint32_t heads_id = a.by_units.div(id);
+  const int u = (int)(id - heads_id * a.units);
+  const uint32_t t = a.by_groups.div(heads_id);
+  const int g = (int)(heads_id - t * a.groups);
   if (t >= a.T) return;
-  const int h0 = (int)(w - t * a.splits) * a.per_warp;
-  const int h1 = min(h0 + a.per_warp, a.heads);
   int64_t pos[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    pos[x] = x < a.axes ? __ldg(a.positions + x * a.axis_stride + t) : 0;
+  const auto in_at = [&](int h) {
+    return h < a.q_heads ? a.q.in + t * a.q.in_ts + h * a.q.in_hs
+                         : a.k.in + t * a.k.in_ts + (h - a.q_heads) * a.k.in_hs;
+  };
+  const auto out_at = [&](int h) {
+    return h < a.q_heads ? a.q.out + t * a.q.out_ts + h * a.q.out_hs
+                         : a.k.out + t * a.k.out_ts + (h - a.q_heads) * a.k.out_hs;
+  };
+  // the two words of the unit (a copied one may lack the second)
+  const bool turned = u * 8 < a.half;
+  const int copy = 2 * a.half + (u - a.half / 8) * 16;
+  const int first = !turned ? copy : kNeox ? u * 8 : u * 16;
+  const int second = turned && kNeox ? first + a.half : first + 8;
+  const bool both = turned || second < 2 * a.half + a.tail * 8;
+  uint4 x[kUnroll], y[kUnroll];
+  const auto load = [&](int h) {
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e)
+      if (h + e * a.groups < a.heads) {
+        const uint16_t* in = in_at(h + e * a.groups);
+        x[e] = *reinterpret_cast<const uint4*>(in + first);
+        if (both) y[e] = *reinterpret_cast<const uint4*>(in + second);
+      }
+  };
+  load(g);
   bool ok = true;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    pos[x] = x < a.axes ? __ldg(a.positions + x * a.axis_stride + t) : 0;
-    ok = ok && pos[x] >= 0 && pos[x] < a.max_pos;
-  }
+  for (int i = 0; i < 4; ++i) ok = ok && pos[i] >= 0 && pos[i] < a.max_pos;
   if (!ok) {
-    if (h0 == 0 && lane == 0) flag_error(a.err, FP4IDX_ERRFLAG_POSITION);
+    if (u == 0 && g == 0) flag_error(a.err, FP4IDX_ERRFLAG_POSITION);
     return;
   }
-  // the angles of unit u's pairs
   float c[8], s[8];
-  const auto angles = [&](int u) {
-    const uint32_t axis = a.axis_bits[u / 2] >> (u % 2 * 16) & 0xffffu;
-    const auto row = [&](uint32_t x) {
-      const int64_t p = x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3];
-      return p * a.half + u * 8;
-    };
-    if (axis == (axis & 3u) * 0x5555u) {  // one axis turns them all
-      const int64_t at = row(axis & 3u);
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 x = ld_f4(a.cos + at + i), y = ld_f4(a.sin + at + i);
-        c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-        s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t at = row(axis >> (2 * i) & 3u) + i;
-        c[i] = __ldg(a.cos + at);
-        s[i] = __ldg(a.sin + at);
-      }
-    }
+  const uint32_t axis = turned ? a.axis_bits[u / 2] >> (u % 2 * 16) & 0xffffu : 0u;
+  const auto row = [&](uint32_t i) {
+    const int64_t p = i == 0 ? pos[0] : i == 1 ? pos[1] : i == 2 ? pos[2] : pos[3];
+    return p * a.half + u * 8;
   };
-  const auto place = [&](int h, const uint16_t*& in, uint16_t*& out) {
-    const bool key = h >= a.q_heads;
-    const int hh = key ? h - a.q_heads : h;
-    const RopeSide& side = key ? a.k : a.q;
-    in = side.in + t * side.in_ts + hh * side.in_hs;
-    out = side.out + t * side.out_ts + hh * side.out_hs;
-  };
-  // the two words of a unit
-  const auto first = [&](int u) { return kNeox ? u * 8 : u * 16; };
-  const int gap = kNeox ? a.half : 8;
-
-  const int end = h1 * a.units;
-  if (kFixed) angles(lane % a.units);
-  for (int j = h0 * a.units + lane; j < end; j += 32 * kUnroll) {
-    uint4 x[kUnroll], y[kUnroll];
+  if (!turned) {
+  } else if (axis == (axis & 3u) * 0x5555u) {  // one axis turns them all
+    const int64_t at = row(axis & 3u);
 #pragma unroll
-    for (int e = 0; e < kUnroll; ++e) {
-      if (j + 32 * e >= end) continue;
-      const int h = (j + 32 * e) / a.units, u = (j + 32 * e) - h * a.units;
-      const uint16_t* in;
-      uint16_t* out;
-      place(h, in, out);
-      x[e] = *reinterpret_cast<const uint4*>(in + first(u));
-      y[e] = *reinterpret_cast<const uint4*>(in + first(u) + gap);
+    for (int i = 0; i < 8; i += 4) {
+      const float4 v = ld_f4(a.cos + at + i), w = ld_f4(a.sin + at + i);
+      c[i] = v.x, c[i + 1] = v.y, c[i + 2] = v.z, c[i + 3] = v.w;
+      s[i] = w.x, s[i + 1] = w.y, s[i + 2] = w.z, s[i + 3] = w.w;
     }
+  } else {
 #pragma unroll
-    for (int e = 0; e < kUnroll; ++e) {
-      if (j + 32 * e >= end) continue;
-      const int h = (j + 32 * e) / a.units, u = (j + 32 * e) - h * a.units;
-      if (!kFixed) angles(u);
-      const uint16_t* in;
-      uint16_t* out;
-      place(h, in, out);
-      uint32_t v[8] = {x[e].x, x[e].y, x[e].z, x[e].w, y[e].x, y[e].y, y[e].z, y[e].w};
-      if constexpr (kNeox) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float2 p = unpack16<kHalf>(v[i]), q = unpack16<kHalf>(v[i + 4]);
-          turn(p.x, q.x, c[2 * i], s[2 * i]);
-          turn(p.y, q.y, c[2 * i + 1], s[2 * i + 1]);
-          v[i] = pack16<kHalf>(p.x, p.y);
-          v[i + 4] = pack16<kHalf>(q.x, q.y);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float2 p = unpack16<kHalf>(v[i]);
-          turn(p.x, p.y, c[i], s[i]);
-          v[i] = pack16<kHalf>(p.x, p.y);
-        }
-      }
-      *reinterpret_cast<uint4*>(out + first(u)) = make_uint4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<uint4*>(out + first(u) + gap) = make_uint4(v[4], v[5], v[6], v[7]);
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = row(axis >> (2 * i) & 3u) + i;
+      c[i] = __ldg(a.cos + at);
+      s[i] = __ldg(a.sin + at);
     }
   }
-  // ---- what is not turned
-  for (int j = h0 * a.tail + lane; j < h1 * a.tail; j += 32) {
-    const int h = j / a.tail, u = j - h * a.tail;
-    const uint16_t* in;
-    uint16_t* out;
-    place(h, in, out);
-    if (in == out) continue;
-    const int at = 2 * a.half + u * 8;
-    *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(in + at);
+  for (int h = g;;) {
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e) {
+      if (h + e * a.groups >= a.heads) continue;
+      if (turned) {
+        uint32_t v[8] = {x[e].x, x[e].y, x[e].z, x[e].w, y[e].x, y[e].y, y[e].z, y[e].w};
+        if constexpr (kNeox) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 p = unpack16<kHalf>(v[i]), q = unpack16<kHalf>(v[i + 4]);
+            turn(p.x, q.x, c[2 * i], s[2 * i]);
+            turn(p.y, q.y, c[2 * i + 1], s[2 * i + 1]);
+            v[i] = pack16<kHalf>(p.x, p.y);
+            v[i + 4] = pack16<kHalf>(q.x, q.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float2 p = unpack16<kHalf>(v[i]);
+            turn(p.x, p.y, c[i], s[i]);
+            v[i] = pack16<kHalf>(p.x, p.y);
+          }
+        }
+        x[e] = make_uint4(v[0], v[1], v[2], v[3]);
+        y[e] = make_uint4(v[4], v[5], v[6], v[7]);
+      }
+      uint16_t* out = out_at(h + e * a.groups);
+      *reinterpret_cast<uint4*>(out + first) = x[e];
+      if (both) *reinterpret_cast<uint4*>(out + second) = y[e];
+    }
+    h += kUnroll * a.groups;
+    if (h >= a.heads) break;
+    load(h);
   }
-}
-
-template <bool kHalf, bool kNeox>
-cudaError_t launch_rope(const RopeArgs& a, unsigned grid, cudaStream_t s) {
-  return 32 % a.units == 0 ? launch_kernel(rope_kernel<kHalf, kNeox, true>, grid, kThreads, 0, s, a)
-                           : launch_kernel(rope_kernel<kHalf, kNeox, false>, grid, kThreads, 0, s,
-                                           a);
 }
 
 }  // namespace
@@ -187,8 +174,8 @@ extern "C" fp4idx_status fp4idx_rope_qk(
   if (num_tokens == 0) return FP4IDX_OK;
   if (!q || !q_out || (k_heads > 0 && (!k || !k_out)) || !positions || !sections || !cos || !sin)
     return FP4IDX_ERR_NULL;
-  if (num_tokens >= (1ll << 31) || q_heads < 1 || q_heads >= (1 << 20) || k_heads < 0 ||
-      k_heads >= (1 << 20) || head_dim < 16 || head_dim > 2 * kMaxPairs || head_dim % 8 ||
+  if (num_tokens >= (1ll << 31) || q_heads < 1 || q_heads > 65535 || k_heads < 0 ||
+      q_heads + k_heads > 65535 || head_dim < 16 || head_dim > 2 * kMaxPairs || head_dim % 8 ||
       rope_dim < 16 || rope_dim > head_dim || rope_dim % 16 || num_axes < 1 || num_axes > 4 ||
       max_pos < 1 || max_pos >= (1ll << 40))
     return FP4IDX_ERR_SHAPE;
@@ -223,7 +210,6 @@ extern "C" fp4idx_status fp4idx_rope_qk(
   a.sin = sin;
   a.max_pos = max_pos;
   a.half = half;
-  a.units = half / 8;
   a.tail = (int32_t)(head_dim - rope_dim) / 8;
   a.T = num_tokens;
   a.err = err_flags;
@@ -239,23 +225,28 @@ extern "C" fp4idx_status fp4idx_rope_qk(
     }
     a.axis_bits[i / 16] |= (uint32_t)axis << (i % 16 * 2);
   }
-  // A warp takes kUnroll units a lane; where the tokens are too few to fill the
-  // GPU so, one unit.
-  int64_t per = 32 * kUnroll / a.units;
-  if (per < 1) per = 1;
-  if (num_tokens * ((a.heads + per - 1) / per) < 4 * kMaxGrid * kWarps) per = 32 / a.units;
-  if (per < 1) per = 1;
-  a.per_warp = (int32_t)per;
-  a.splits = (int32_t)((a.heads + per - 1) / per);
-  const int64_t blocks = (num_tokens * a.splits + kWarps - 1) / kWarps;
-  if (blocks >= (1ll << 31)) return FP4IDX_ERR_SHAPE;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // In place nothing needs to be copied.
+  const bool in_place = q == q_out && (k_heads == 0 || k == k_out);
+  if (in_place) a.tail = 0;
+  a.units = half / 8 + (a.tail + 1) / 2;
+  // A thread takes 8 heads (angles read once for 512 bytes of rows); where the
+  // tokens are too few to fill the GPU so, fewer.
+  const int64_t ids = num_tokens * a.units;
+  int64_t per = 2 * kUnroll;
+  while (per > 1 && ids * ((a.heads + per - 1) / per) < (int64_t)kMaxGrid * 1024) per /= 2;
+  a.groups = (int32_t)((a.heads + per - 1) / per);
+  a.by_units = make_fastdiv((uint32_t)a.units);
+  a.by_groups = make_fastdiv((uint32_t)a.groups);
+  const int64_t blocks = (ids * a.groups + kThreads - 1) / kThreads;
+  if (ids * a.groups >= (1ll << 32) - kThreads) return FP4IDX_ERR_SHAPE;
   const bool h = dtype == FP4IDX_FP16;
-  const unsigned grid = (unsigned)blocks;
-  const cudaError_t st = rope_style == FP4IDX_ROPE_NEOX
-                             ? (h ? launch_rope<true, true>(a, grid, s)
-                                  : launch_rope<false, true>(a, grid, s))
-                             : (h ? launch_rope<true, false>(a, grid, s)
-                                  : launch_rope<false, false>(a, grid, s));
+  auto* kern = rope_style == FP4IDX_ROPE_NEOX
+                   ? (h ? rope_kernel<true, true> : rope_kernel<false, true>)
+                   : (h ? rope_kernel<true, false> : rope_kernel<false, false>);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t st = cudaLaunchKernelEx(&cfg, kern, a);
   return st == cudaSuccess ? FP4IDX_OK : FP4IDX_ERR_CUDA;
 }
