@@ -139,7 +139,7 @@ __device__ __forceinline__ uint32_t count_of(const int32_t* free_count, int64_t 
 }
 
 __global__ __launch_bounds__(kThreads) void extend_kernel(const ExtendArgs a) {
-  extern __shared__ uint32_t smem[];
+  extern __shared__ __align__(16) uint32_t smem[];
   __shared__ uint32_t part[3][32];
   const int tid = threadIdx.x, threads = blockDim.x, chunk = threads * kEach;
   uint32_t* const ends = smem;            // of a sequence's tokens, in the call
@@ -183,17 +183,23 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(const ExtendArgs a) {
       upto = capped(upto, min(need[j], page_cap), page_cap);
       const bool served = fits[j] && (need[j] == 0 || upto <= count);
       if (served && need[j] > 0) most = upto;
-      ends[tid * kEach + j] = min(end[j], T);
-      first[tid * kEach + j] = served ? (uint32_t)old[j] : ~0u;
-      taken[tid * kEach + j] = before;
+      end[j] = min(end[j], T);
+      start[j] = min(start[j], T);
+      need[j] = before;
+      // (from here on the length after the call, and the first new token's position)
+      add[j] = served ? old[j] + add[j] : old[j];
+      old[j] = served ? old[j] : -1;
       if (b + j < a.batch) {
         full = full || !served;
         if (turn % ctas == rank) {
-          if (a.q_starts) a.q_starts[b + j] = (int32_t)min(start[j], T);
-          if (a.context) a.context[b + j] = served ? old[j] + add[j] : old[j];
+          if (a.q_starts) a.q_starts[b + j] = (int32_t)start[j];
+          if (a.context) a.context[b + j] = add[j];
         }
       }
     }
+    reinterpret_cast<uint4*>(ends)[tid] = make_uint4(end[0], end[1], end[2], end[3]);
+    reinterpret_cast<int4*>(first)[tid] = make_int4(old[0], old[1], old[2], old[3]);
+    reinterpret_cast<uint4*>(taken)[tid] = make_uint4(need[0], need[1], need[2], need[3]);
     if (full && turn % ctas == rank) flag_error(a.err, FP4IDX_ERRFLAG_FULL);
     most = __reduce_max_sync(kFull, most);
     if (tid % 32 == 0) part[2][tid / 32] = most;
@@ -207,10 +213,35 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(const ExtendArgs a) {
     const uint32_t t1 = min(done, T);
     for (uint32_t g = t0 / 4 + rank * threads + tid; g < (t1 + 3) / 4; g += ctas * threads) {
       const uint32_t t = g * 4;
+      int s = find(ends, n, max(t, t0));
+      const bool whole = a.vec && t >= t0 && t + 3 < t1;
+      {  // four tokens of one page, as most are in a prompt
+        const uint32_t f = first[s], p = f + (t - (s > 0 ? ends[s - 1] : t0));
+        if (whole && ends[s] > t + 3 && f != ~0u && p % kPage <= kPage - 4) {
+          const uint32_t idx = p / kPage, held = pages_of(f);
+          int32_t* const place = a.table + (b0 + s) * a.tstride + idx;
+          const int32_t page =
+              idx < held ? *place : a.free_pages[count - 1 - (taken[s] + (idx - held))];
+          if (idx >= held && p % kPage == 0) *place = page;
+          const int64_t slot = (int64_t)page * kPage + p % kPage;
+          const int32_t id = (int32_t)b0 + s;
+          if (a.slots) {
+            reinterpret_cast<longlong2*>(a.slots + t)[0] = make_longlong2(slot, slot + 1);
+            reinterpret_cast<longlong2*>(a.slots + t)[1] = make_longlong2(slot + 2, slot + 3);
+          }
+          if (a.positions) {
+            reinterpret_cast<longlong2*>(a.positions + t)[0] = make_longlong2(p, p + 1);
+            reinterpret_cast<longlong2*>(a.positions + t)[1] = make_longlong2(p + 2, p + 3);
+          }
+          if (a.seq_ids) *reinterpret_cast<int4*>(a.seq_ids + t) = make_int4(id, id, id, id);
+          if (a.row_lens)
+            *reinterpret_cast<int4*>(a.row_lens + t) = make_int4(p + 1, p + 2, p + 3, p + 4);
+          continue;
+        }
+      }
       int32_t seq[4], pos[4];  // pos -1: nothing
       const int32_t* from[4];  // its page's number
       int32_t* entry[4];       // its place in the table, if it is new and begins here
-      int s = -1;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t x = t + j;
@@ -219,7 +250,6 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(const ExtendArgs a) {
         from[j] = nullptr;
         entry[j] = nullptr;
         if (x < t0 || x >= t1) continue;
-        if (s < 0) s = find(ends, n, x);
         if (ends[s] <= x && ends[++s] <= x) s = find(ends, n, x);
         seq[j] = (int32_t)b0 + s;
         const uint32_t f = first[s];
@@ -240,9 +270,8 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(const ExtendArgs a) {
       for (int j = 0; j < 4; ++j) {
         slot[j] = pos[j] < 0 ? -1 : (int64_t)page[j] * kPage + pos[j] % kPage;
         if (entry[j]) *entry[j] = page[j];
-        pos[j] = max(pos[j], -1);
       }
-      if (a.vec && t >= t0 && t + 3 < t1) {
+      if (whole) {
         if (a.slots) {
           reinterpret_cast<longlong2*>(a.slots + t)[0] = make_longlong2(slot[0], slot[1]);
           reinterpret_cast<longlong2*>(a.slots + t)[1] = make_longlong2(slot[2], slot[3]);
@@ -353,8 +382,10 @@ __global__ __launch_bounds__(kThreads) void release_kernel(const ReleaseArgs a) 
 template <typename Args>
 fp4idx_status launch_cluster(void (*kern)(Args), int64_t batch, int64_t elements, int words,
                              cudaStream_t stream, const Args& a) {
-  const bool many = elements > 4 * kThreads;
-  const int threads = !many && batch <= 256 * kEach ? 256 : kThreads;
+  // (a CTA's threads take 150 instructions for a token of its own: 4,096 tokens of
+  // one sequence 9.2 us in one CTA)
+  const bool many = elements > kThreads;
+  const int threads = elements <= 8 * kThreads && batch <= 256 * kEach ? 256 : kThreads;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = many ? kClusterMax : 1;
@@ -418,7 +449,7 @@ extern "C" fp4idx_status fp4idx_batch_extend(
   a.vec = aligned(slot_mapping, 16) && aligned(positions, 16) && aligned(seq_ids, 16) &&
           aligned(row_lens, 16);
   a.err = err_flags;
-  static SmemOnce once;
+  static SmemOnce once;  // (48 KB beside the static words)
   if (!once.set(extend_kernel, kChunk * 3 * 4)) return FP4IDX_ERR_CUDA;
   return launch_cluster(extend_kernel, batch, num_tokens, 3, static_cast<cudaStream_t>(stream), a);
 }

@@ -1109,6 +1109,27 @@ class BatchMaps(NamedTuple):
 def _pool(first, second, names, block_table, free_pages, free_count):
     """Checks of two vectors of lengths and the page pool; (device index, batch,
     the pool's C arguments)."""
+    i32 = _torch().int32
+    try:  # the usual call in one test; what fails it is looked at piece by piece
+        batch, pages = block_table.shape
+        st, dev = block_table.stride(), block_table.get_device()
+        n, = free_pages.shape
+        if (block_table.dtype is first.dtype is second.dtype is free_pages.dtype is
+                free_count.dtype is i32 and dev >= 0 and
+                first.get_device() == second.get_device() == free_pages.get_device() ==
+                free_count.get_device() == dev and
+                first.shape == second.shape == (batch,) and free_count.shape == (1,) and
+                first.is_contiguous() and second.is_contiguous() and
+                free_pages.is_contiguous() and batch > 1 and pages > 1 and st[1] == 1 and
+                st[0] >= pages):
+            return dev, batch, (block_table.data_ptr(), st[0], pages, free_pages.data_ptr(),
+                                free_count.data_ptr(), n)
+    except (AttributeError, ValueError):
+        pass
+    return _pool_slow(first, second, names, block_table, free_pages, free_count)
+
+
+def _pool_slow(first, second, names, block_table, free_pages, free_count):
     torch = _torch()
     i32 = torch.int32
     dev = block_table.get_device() if isinstance(block_table, torch.Tensor) else -1
@@ -1132,6 +1153,9 @@ def _pool(first, second, names, block_table, free_pages, free_count):
                         free_pages.data_ptr(), free_count.data_ptr(), free_pages.shape[0])
 
 
+_NO_MAPS = (None,) * 6
+
+
 def batch_extend(cached_lens, new_lens, block_table, free_pages, free_count, num_tokens: int, *,
                  q_starts=None, context_lens=None, slot_mapping=None, positions=None, seq_ids=None,
                  row_lens=None, err_flags=None, stream=None) -> BatchMaps:
@@ -1148,19 +1172,27 @@ def batch_extend(cached_lens, new_lens, block_table, free_pages, free_count, num
     if num_tokens < 0:
         raise ValueError("num_tokens must not be negative")
     given = (q_starts, context_lens, slot_mapping, positions, seq_ids, row_lens)
-    i32, i64 = torch.int32, torch.int64
-    maps = []
     with _on(stream):
-        for t, n, dt, name in zip(given, (batch + 1, batch, *[num_tokens] * 4),
-                                  (i32, i32, i64, i64, i32, i32), BatchMaps._fields):
-            if t is None:
-                t = torch.empty(n, dtype=dt, device=block_table.device)
-            else:
-                _fits(t, dt, 1, dev, name)
-                _dense(t, (n,), name)
-            maps.append(t)
+        i32, i64, empty = torch.int32, torch.int64, torch.empty
+        if given == _NO_MAPS:  # (six allocations cost less than views of two)
+            at = block_table.device
+            maps = (empty(batch + 1, dtype=i32, device=at), empty(batch, dtype=i32, device=at),
+                    empty(num_tokens, dtype=i64, device=at),
+                    empty(num_tokens, dtype=i64, device=at),
+                    empty(num_tokens, dtype=i32, device=at),
+                    empty(num_tokens, dtype=i32, device=at))
+        else:
+            maps = []
+            for t, n, dt, name in zip(given, (batch + 1, batch, *[num_tokens] * 4),
+                                      (i32, i32, i64, i64, i32, i32), BatchMaps._fields):
+                if t is None:
+                    t = empty(n, dtype=dt, device=block_table.device)
+                else:
+                    _fits(t, dt, 1, dev, name)
+                    _dense(t, (n,), name)
+                maps.append(t)
     _call(_lib.fp4idx_batch_extend, dev, stream, cached_lens.data_ptr(), new_lens.data_ptr(),
-          *pool, *(t.data_ptr() for t in maps), batch, num_tokens, _flags(err_flags, dev))
+          *pool, *[t.data_ptr() for t in maps], batch, num_tokens, _flags(err_flags, dev))
     return BatchMaps(*maps)
 
 
@@ -1185,6 +1217,16 @@ def _sections(sections):
     return (ctypes.c_int32 * len(sections))(*sections)
 
 
+def _out16(t, q, T, H, D, dev, name):
+    """(token stride, head stride) of an output of q's type, [T, H, D]."""
+    if t.dtype is not q.dtype:
+        raise TypeError(f"{name} must be {q.dtype}, got {t.dtype}")
+    got = _rows16(t, H, D, dev, name)
+    if len(t) != T:
+        raise ValueError(f"{name} must have T rows")
+    return got
+
+
 def rope_qk(q, k, positions, cos, sin, *, rope_style="neox", sections=None,
             interleaved_axes: bool = False, q_out=None, k_out=None, err_flags=None, stream=None):
     """Rotary positions of queries and keys -> (q_out, k_out).  q, k bf16 or fp16
@@ -1204,7 +1246,7 @@ def rope_qk(q, k, positions, cos, sin, *, rope_style="neox", sections=None,
     if k is not None:
         if _type16(k, "k") != dt:
             raise TypeError("q and k must have the same dtype")
-        if k.dim() != 3 or k.shape[0] != T:
+        if k.dim() != 3 or len(k) != T:
             raise ValueError("k must be [T, heads, D] with q's tokens")
         Hk = k.shape[1]
         ks = _rows16(k, Hk, D, dev, "k")
@@ -1212,38 +1254,38 @@ def rope_qk(q, k, positions, cos, sin, *, rope_style="neox", sections=None,
         raise ValueError("k_out without k")
     _fits(cos, torch.float32, 2, dev, "cos")
     _fits(sin, torch.float32, 2, dev, "sin")
-    _dense(cos, cos.shape, "cos")
-    _dense(sin, cos.shape, "sin")
-    max_pos, half = cos.shape
-    axes = 1
-    if isinstance(positions, torch.Tensor) and positions.dim() == 2:
-        axes = positions.shape[0]
-        if sections is None and axes > 1:
-            raise ValueError("positions of several axes need sections")
-    _fits(positions, torch.int64, positions.dim() if axes > 1 or (
-        isinstance(positions, torch.Tensor) and positions.dim() == 2) else 1, dev, "positions")
-    if positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
+    shape = cos.shape
+    _dense(cos, shape, "cos")
+    _dense(sin, shape, "sin")
+    max_pos, half = shape
+    several = getattr(positions, "ndim", 1) == 2
+    _fits(positions, torch.int64, 2 if several else 1, dev, "positions")
+    st = positions.stride()
+    if positions.shape[-1] != T or (T > 1 and st[-1] != 1):
         raise ValueError("positions must be [T] or [axes, T] with unit token stride")
-    sections = (half,) if sections is None else tuple(int(n) for n in sections)
-    if len(sections) != axes:
+    axes = len(positions) if several else 1
+    if sections is None:
+        if axes > 1:
+            raise ValueError("positions of several axes need sections")
+        sections = (half,)
+    elif len(sections) != axes:
         raise ValueError("sections must have an entry for each axis of positions")
+    qo, ko, kp, kop = (Hq * D, D), (Hk * D, D), None, None
     with _on(stream):
         if q_out is None:
             q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-        if k_out is None and k is not None:
-            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device)
-    _fits(q_out, q.dtype, 3, dev, "q_out")
-    qo, ko = _rows16(q_out, Hq, D, dev, "q_out"), (0, 0)
-    if q_out.shape[0] != T:
-        raise ValueError("q_out must have q's shape")
-    if k is not None:
-        _fits(k_out, q.dtype, 3, dev, "k_out")
-        ko = _rows16(k_out, Hk, D, dev, "k_out")
-        if k_out.shape[0] != T:
-            raise ValueError("k_out must have k's shape")
-    _call(_lib.fp4idx_rope_qk, dev, stream, q.data_ptr(), *qs, q_out.data_ptr(), *qo, Hq,
-          k.data_ptr() if Hk else None, *ks, k_out.data_ptr() if Hk else None, *ko, Hk, dt, D,
-          positions.data_ptr(), positions.stride(0) if axes > 1 else T, _sections(sections), axes,
+        else:
+            qo = _out16(q_out, q, T, Hq, D, dev, "q_out")
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device)
+            else:
+                ko = _out16(k_out, q, T, Hk, D, dev, "k_out")
+            if Hk:
+                kp, kop = k.data_ptr(), k_out.data_ptr()
+    _call(_lib.fp4idx_rope_qk, dev, stream, q.data_ptr(), *qs, q_out.data_ptr(), *qo, Hq, kp, *ks,
+          kop, *ko, Hk, dt, D, positions.data_ptr(), st[0] if several and axes > 1 else T,
+          _sections(tuple(sections)), axes,
           AXES_INTERLEAVED if interleaved_axes else AXES_SECTIONS, cos.data_ptr(), sin.data_ptr(),
           max_pos, 2 * half, rope_style_code(rope_style), T, _flags(err_flags, dev))
     return q_out, k_out
