@@ -537,7 +537,8 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
       if (says_all) mbar_arrive(bar(B::kEmpty + (2 * all - 1) % kRing));
       if (ok && !idle) {
         fence_after();
-        const bool some = M != -INFINITY;
+        // (scores that are all NaN move no reference)
+        const bool some = M != -INFINITY || l != l;
         const float inv = some ? __frcp_rn(l) : 0.0f;
         const float lse2 = some ? M - kShift + __log2f(l) : -INFINITY;
         // four lanes turn their rows' 64 bytes into four times 64 bytes of a row: a
@@ -874,7 +875,15 @@ __global__ __launch_bounds__(256) void join_prompt_kernel(const __grid_constant_
   for (int k = 0; k < kRows; ++k) {
     if (r0 + k >= m.rows) continue;
     const int r = m.row0 + r0 + k, tok = (int)a.by_g.div(r);
-    const bool some = top[k] != -INFINITY;
+    bool some = top[k] != -INFINITY;
+    if (!some)  // no key, or parts that are all NaN
+      for (int f = 0; f < n; ++f) {
+        const float x = a.part_lse[slot(f) * kItemRows + r0 + k];
+        if (x != x) {
+          some = true;
+          den[k] = x;
+        }
+      }
     const float inv = some ? __frcp_rn(den[k]) : 0.0f;
     const int64_t orow = (int64_t)(m.q0 + tok) * a.Hq + cut.z * a.G + (r - tok * a.G);
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * kV);

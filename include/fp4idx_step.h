@@ -123,7 +123,8 @@ enum {
  *   q_out, k_out  the same, with strides of their own.  q_out may be q with q's
  *                 strides (in place), and k_out k; any other overlap of an
  *                 output with an input is the caller's error.
- *   head_dim      a multiple of 8, at most 1024;  rope_dim a multiple of 16, at
+ *   q_heads       at least 1; q_heads + k_heads at most 65535.
+ *   head_dim      a multiple of 8, 16 .. 1024;  rope_dim a multiple of 16, at
  *                 most head_dim.
  *   positions     int64, axis a of token t at a*axis_stride + t.
  *   sections      HOST int32 [num_axes], not negative, their sum R / 2; read
@@ -158,7 +159,7 @@ fp4idx_status fp4idx_rope_qk(const void* q, int64_t q_token_stride, int64_t q_he
  *
  * Products are exact in the tensor core, the softmax and both sums fp32;
  * probabilities are rounded to the elements' type before the product with the
- * values: bf16 by 2^-9 of themselves, fp16 by 2^-12, or 2^-35 of the row's
+ * values: bf16 by 2^-8 of themselves, fp16 by 2^-11 or 2^-35 of the row's
  * largest.  A score carries fp32's relative error into its exponent, so |x_s| is
  * to stay below 2^20.
  *
