@@ -858,8 +858,10 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(const AttnArgs a) {
   }
 }
 
-// Joins the partial outputs of the items that a share's end cut (join_rows).
-// Blocks (CTA whose share begins the item, 32 of its rows), four rows a warp.
+// Joins the partial outputs of the items that a share's end cut: weights
+// 2^(lse - max), in the order of the CTAs, applied in two halves (a part of weight
+// 2^-126 counts where its values are as much larger).  Blocks (CTA whose share
+// begins the item, 32 of its rows), four rows a warp.
 template <int D>
 __global__ __launch_bounds__(256) void join_tiles_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -876,10 +878,30 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(const AttnArgs a) {
   const int r0 = blockIdx.x % kBlocks * 32 + threadIdx.x / 32 * kRows;
   if (r0 >= m.rows) return;
   float top[kRows], den[kRows], o[kRows][kV];
-  const auto at = [&](int64_t place, int row) {
-    return (place * kItemRows + row) * D + lane * kV;
-  };
-  join_rows<D, kRows, kItemRows>(a.part_out, a.part_lse, n, r0, m.rows, slot, at, top, den, o);
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    top[k] = -INFINITY;
+    den[k] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) o[k][j] = 0.0f;
+  }
+#pragma unroll 2
+  for (int f = 0; f < n; ++f)
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (r0 + k < m.rows) top[k] = fmaxf(top[k], a.part_lse[slot(f) * kItemRows + r0 + k]);
+#pragma unroll 2
+  for (int f = 0; f < n; ++f)
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (r0 + k >= m.rows || top[k] == -INFINITY) continue;
+      const int64_t row = slot(f) * kItemRows + r0 + k;
+      const float half = exp2_approx(0.5f * (a.part_lse[row] - top[k]));
+      den[k] = fmaf(half, half, den[k]);
+#pragma unroll
+      for (int j = 0; j < kV; ++j)
+        o[k][j] = fmaf(a.part_out[row * D + lane * kV + j] * half, half, o[k][j]);
+    }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     const int r = m.row0 + r0 + k;

@@ -35,7 +35,9 @@
 // 256 + D.
 // The items and their tiles form one list, cut into equal shares, one per CTA,
 // from the lengths alone; an item cut by a share's end leaves normalised
-// partial outputs, joined by a second kernel in a fixed order.
+// partial outputs, joined by a second kernel in a fixed order.  Where no item has
+// more than kWhole tiles, an item belongs to the share that holds its first tile
+// instead, and there is no second kernel.
 // Every wait is bounded (1 s) and a shared abort flag stops every role; copies
 // and MMAs in flight are waited for before the CTA ends.
 
@@ -83,6 +85,7 @@ struct PromptArgs {
   int32_t batch, Tq, Tk, Hq, Hkv, G;
   FastDiv by_g;
   int32_t rc_max;    // row chunks of a sequence, at most
+  int32_t whole;     // items are not cut
   int32_t withhold;  // testing: tile of CTA 0 that is never loaded (-1: none)
   float scale_log2;
   uint16_t* out;
@@ -135,7 +138,8 @@ __device__ __forceinline__ int key_of_tile(const Item& m, int t) {
 // its output wait for one another.  Measured 8,500 cycles against 2,900 a tile (D =
 // 128); shares of equal tiles left the CTA with the shortest items 1.5 times the
 // others' time.
-constexpr int kStart = 3;
+constexpr int kStart = 2;
+constexpr int kWhole = 4;
 
 // Where element d (a multiple of 4, and up to 3 more) of an item's row lies in
 // partial output `place`: the rows of four elements together, so that a warp
@@ -149,7 +153,8 @@ __device__ __forceinline__ int64_t part_at(int64_t place, int d, int row) {
 // the item's tiles, a unit each.  It is cut into equal shares, one per CTA.
 struct Share {
   int64_t s0, s1, total;
-  int b, rc, head, off;  // the item of unit s0, and the unit in it
+  int b, rc, head;       // the item of unit s0
+  int off, units;        // that unit in it; its units
   int grid;              // CTAs with a share
 };
 
@@ -204,7 +209,8 @@ __device__ __forceinline__ void locate_share(const PromptArgs& a, Share& sh) {
   }
   // shares of at least four tiles, but every item may have a CTA of its own
   const int64_t most = gridDim.x;
-  const int64_t grid = min(max(total / 4, min(n * a.Hkv, most)), most);
+  const int64_t each_own = min(n * a.Hkv, most);
+  const int64_t grid = a.whole ? each_own : max(min(total / 4, most), each_own);
   const int64_t s0 = blockIdx.x < grid ? total * blockIdx.x / grid : 0;
   const int64_t s1 = blockIdx.x < grid ? total * (blockIdx.x + 1) / grid : 0;
   const int64_t from = base + incl - own;
@@ -225,6 +231,7 @@ __device__ __forceinline__ void locate_share(const PromptArgs& a, Share& sh) {
           sh.rc = rc;
           sh.head = (int)((s0 - at) / units);
           sh.off = (int)((s0 - at) % units);
+          sh.units = units;
           break;
         }
         at += u;
@@ -382,8 +389,10 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // joins as CTAs end
   locate_share(a, ctl.share);
   const Share& share = ctl.share;
-  // (a share may be empty, or end before its first item's first tile)
-  if (share.s0 >= share.s1 || share.off + (share.s1 - share.s0) <= kStart) {
+  // (a share may be empty, or end before the first tile of its first item)
+  const int64_t begin = share.s0 - share.off;  // of that
+  const bool theirs = a.whole && share.off > kStart;
+  if (share.s0 >= share.s1 || begin + (theirs ? share.units : 0) + kStart >= share.s1) {
     if (tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
@@ -754,10 +763,25 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
     }
   } else if (warp == kLoadWarp) {
     // -------------------------------------------------- work list and tiles
-    int b = share.b, rc = share.rc, head = share.head, off = share.off;
-    int64_t at = share.s0;
-    bool more = true;
+    int b = share.b, rc = share.rc, head = share.head;
+    int64_t at = begin;  // the item's first unit
     int4 cut = make_int4(0, 0, 0, 0);
+    bool more = true;
+    const auto next_item = [&]() {
+      if (++head < a.Hkv) return;
+      head = 0;
+      Item it;
+      do {
+        if (++rc == a.rc_max) {
+          rc = 0;
+          ++b;
+        }
+      } while (!item_of(a, b, rc, it));
+    };
+    if (theirs) {
+      at += share.units;
+      next_item();
+    }
     // (testing hook, see fp4idx_test_withhold_next: a tile that is not loaded)
     const uint32_t held = blockIdx.x == 0 && a.withhold >= 0 ? 2u * a.withhold : 0xffffffffu;
     bool ok = true;
@@ -768,17 +792,16 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
       item_of(a, b, rc, sg.m);
       sg.head = head;
       const int units = sg.m.nt + kStart;
-      const int end = (int)min((int64_t)units, off + (share.s1 - at));  // above kStart
-      sg.t0 = max(off - kStart, 0);
-      sg.t1 = end - kStart;
+      const int64_t tiles = at + kStart;  // the unit of the first one
+      sg.t0 = a.whole ? 0 : (int)max(share.s0 - tiles, (int64_t)0);
+      sg.t1 = a.whole ? sg.m.nt : (int)min(share.s1 - tiles, (int64_t)sg.m.nt);
       sg.whole = sg.t0 == 0 && sg.t1 == sg.m.nt;
       sg.part = 2 * blockIdx.x + (sg.t0 == 0 && i > 0 ? 1 : 0);
       if (!sg.whole && sg.t0 == 0)  // the first fragment of a cut item
         cut = make_int4(b, rc, head,
-                        (cta_of(at - off + units - 1, share) - (int)blockIdx.x + 1) * 2 +
-                            (sg.part & 1));
-      at += end - off;
-      more = share.s1 - at > kStart;  // a tile of the next item
+                        (cta_of(at + units - 1, share) - (int)blockIdx.x + 1) * 2 + (sg.part & 1));
+      at += units;
+      more = at + kStart < share.s1;  // the next item's first tile
       sg.more = more;
       if (lane == 0) {
         ctl.segs[i % kSegRing] = sg;
@@ -807,17 +830,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
           __syncwarp();
         }
       }
-      off = 0;
-      if (++head == a.Hkv && more) {
-        head = 0;
-        Item it;
-        do {
-          if (++rc == a.rc_max) {
-            rc = 0;
-            ++b;
-          }
-        } while (!item_of(a, b, rc, it));
-      }
+      if (more) next_item();
     }
     if (lane == 0) a.cuts[blockIdx.x] = cut;
   }
@@ -851,48 +864,68 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
   }
 }
 
-// Joins the partial outputs of the items that a share's end cut (join_rows).
-// Blocks (CTA whose share begins the item, 32 of its rows), four rows a warp.
+// Joins the partial outputs of the items that a share's end cut: weights
+// 2^(lse - max), applied in two halves (a part of weight 2^-126 counts where its
+// values are as much larger), in the order of the CTAs.  A warp takes 32 rows, a row a lane, and
+// 16 elements of each: it reads partial outputs in runs of 512 bytes and writes 32
+// bytes a row.  Blocks (CTA whose share begins the item, 4,096 of
+// its elements).
 template <int D, bool kHalf>
 __global__ __launch_bounds__(256) void join_prompt_kernel(const __grid_constant__ PromptArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kBlocks = kItemRows / 32;
-  const int cta = blockIdx.x / kBlocks;
+  constexpr int kParts = D / 16, kRowsOf = 8 / kParts * 32;  // warps of a row; rows of a block
+  const int cta = blockIdx.x / (kItemRows / kRowsOf);
   const int4 cut = a.cuts[cta];
   const int n = cut.w / 2;
   if (n < 2) return;
   Item m;
   item_of(a, cut.x, cut.y, m);
-  const int lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int row = blockIdx.x % (kItemRows / kRowsOf) * kRowsOf + warp / kParts * 32 + lane;
+  const int d = warp % kParts * 16;
+  if (row >= m.rows) return;
   const auto slot = [&](int f) { return (int64_t)2 * (cta + f) + (f == 0 ? cut.w & 1 : 0); };
-  constexpr int kV = D / 32, kRows = 4;
-  const int r0 = blockIdx.x % kBlocks * 32 + threadIdx.x / 32 * kRows;
-  if (r0 >= m.rows) return;
-  float top[kRows], den[kRows], o[kRows][kV];
-  const auto at = [&](int64_t place, int row) { return part_at<D>(place, lane * kV, row); };
-  join_rows<D, kRows, kItemRows>(a.part_out, a.part_lse, n, r0, m.rows, slot, at, top, den, o);
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    if (r0 + k >= m.rows) continue;
-    const int r = m.row0 + r0 + k, tok = (int)a.by_g.div(r);
-    bool some = top[k] != -INFINITY;
-    if (!some)  // no key, or parts that are all NaN
-      for (int f = 0; f < n; ++f) {
-        const float x = a.part_lse[slot(f) * kItemRows + r0 + k];
-        if (x != x) {
-          some = true;
-          den[k] = x;
-        }
-      }
-    const float inv = some ? __frcp_rn(den[k]) : 0.0f;
-    const int64_t orow = (int64_t)(m.q0 + tok) * a.Hq + cut.z * a.G + (r - tok * a.G);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * kV);
-#pragma unroll
-    for (int j = 0; j < kV; j += 2)
-      dst[j / 2] = pack16<kHalf>(o[k][j] * inv, o[k][j + 1] * inv);
-    if (a.lse && lane == 0)
-      a.lse[orow] = some ? (top[k] + __log2f(den[k])) * kLn2 : -INFINITY;
+  float top = -INFINITY;
+  bool nan = false;
+#pragma unroll 4
+  for (int f = 0; f < n; ++f) {
+    const float x = a.part_lse[slot(f) * kItemRows + row];
+    nan = nan || x != x;
+    top = fmaxf(top, x);
   }
+  // (parts that are all NaN have no largest)
+  const bool some = top != -INFINITY || nan;
+  const float ref = or_zero(top);
+  float den = 0.0f, o[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) o[j] = 0.0f;
+#pragma unroll 4
+  for (int f = 0; f < n; ++f) {
+    const int64_t place = slot(f);
+    const float w = exp2_approx(0.5f * (a.part_lse[place * kItemRows + row] - ref));
+    float4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = *reinterpret_cast<const float4*>(a.part_out + part_at<D>(place, d + 4 * j, row));
+    den = fmaf(w, w, den);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[4 * j] = fmaf(v[j].x * w, w, o[4 * j]);
+      o[4 * j + 1] = fmaf(v[j].y * w, w, o[4 * j + 1]);
+      o[4 * j + 2] = fmaf(v[j].z * w, w, o[4 * j + 2]);
+      o[4 * j + 3] = fmaf(v[j].w * w, w, o[4 * j + 3]);
+    }
+  }
+  const float inv = some ? __frcp_rn(den) : 0.0f;
+  const int r = m.row0 + row, tok = (int)a.by_g.div(r);
+  const int64_t orow = (int64_t)(m.q0 + tok) * a.Hq + cut.z * a.G + (r - tok * a.G);
+  uint32_t u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) u[j] = pack16<kHalf>(o[2 * j] * inv, o[2 * j + 1] * inv);
+  uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + d);
+  dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
+  dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  if (a.lse && d == 0) a.lse[orow] = some ? (top + __log2f(den)) * kLn2 : -INFINITY;
 }
 
 template <int D, bool kHalf>
@@ -902,8 +935,9 @@ fp4idx_status launch_prompt(const PromptArgs& a, int grid, cudaStream_t stream) 
   if (launch_kernel(prompt_kernel<D, kHalf>, (unsigned)grid, kThreads, smem_bytes(D), stream, a) !=
       cudaSuccess)
     return FP4IDX_ERR_CUDA;
-  return launch_after(join_prompt_kernel<D, kHalf>, (unsigned)(grid * (kItemRows / 32)), 256,
-                      stream, a) == cudaSuccess
+  if (a.whole) return FP4IDX_OK;
+  return launch_after(join_prompt_kernel<D, kHalf>, (unsigned)(grid * (D / 16)), 256, stream,
+                      a) == cudaSuccess
              ? FP4IDX_OK
              : FP4IDX_ERR_CUDA;
 }
@@ -1080,6 +1114,14 @@ extern "C" fp4idx_status fp4idx_prompt_attention(
   a.by_g = make_fastdiv((uint32_t)a.G);
   const int64_t most_q = max_q < q_tokens ? max_q : q_tokens;
   a.rc_max = (int32_t)((most_q * a.G + kItemRows - 1) / kItemRows);
+  // tiles of an item, at most
+  int64_t tiles = (max_k + kTile - 1) / kTile;
+  if (a.window > 0) {
+    const int64_t seen = (a.window + kItemRows / a.G + 2 * kTile) / kTile +
+                         (a.sinks + kTile - 1) / kTile;
+    if (seen < tiles) tiles = seen;
+  }
+  a.whole = tiles <= kWhole;
   a.withhold = -1;
   a.scale_log2 = softmax_scale * kLog2e;
   a.out = static_cast<uint16_t*>(out);

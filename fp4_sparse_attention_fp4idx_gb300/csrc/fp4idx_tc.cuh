@@ -1,6 +1,5 @@
 // fp4idx_tc.cuh -- what the attention kernels on tcgen05.mma share: bounded
-// waits, descriptors, MMA and TMEM instructions, masks of 32 keys, and the join
-// of an item's partial outputs.
+// waits, descriptors, MMA and TMEM instructions, masks of 32 keys.
 #pragma once
 
 #include "fp4idx_attention_common.cuh"
@@ -176,44 +175,6 @@ __device__ __forceinline__ void set_regs_up() {
 template <int N>
 __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// One row's partial outputs of a cut item joined: weights 2^(lse - max), in the
-// order of the parts, applied in two halves (a part of weight 2^-126 counts
-// where its values are as much larger).  Rows r0 .. r0 + kRows - 1 of an item of
-// kItemRows, D / 32 elements a lane; slot(f) is part f's place and at(slot, row)
-// where the lane's elements of a row in it are.
-template <int D, int kRows, int kItemRows, typename Slot, typename At>
-__device__ __forceinline__ void join_rows(const float* part_out, const float* part_lse, int n,
-                                          int r0, int rows, Slot slot, At at,
-                                          float (&top)[kRows], float (&den)[kRows],
-                                          float (&o)[kRows][D / 32]) {
-  constexpr int kV = D / 32;
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    top[k] = -INFINITY;
-    den[k] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kV; ++j) o[k][j] = 0.0f;
-  }
-#pragma unroll 2
-  for (int f = 0; f < n; ++f)
-#pragma unroll
-    for (int k = 0; k < kRows; ++k)
-      if (r0 + k < rows) top[k] = fmaxf(top[k], part_lse[slot(f) * kItemRows + r0 + k]);
-#pragma unroll 2
-  for (int f = 0; f < n; ++f)
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      if (r0 + k >= rows || top[k] == -INFINITY) continue;
-      const int64_t place = slot(f), from = at(place, r0 + k);
-      const float half =
-          exp2_approx(0.5f * (part_lse[place * kItemRows + r0 + k] - top[k]));
-      den[k] = fmaf(half, half, den[k]);
-#pragma unroll
-      for (int j = 0; j < kV; ++j)
-        o[k][j] = fmaf(part_out[from + j] * half, half, o[k][j]);
-    }
 }
 
 }  // namespace fp4idx_impl
