@@ -51,7 +51,7 @@ namespace fp4idx_impl {
 namespace {
 
 constexpr int kTile = 128;  // keys of a tile
-constexpr int kHalfRows = 128;
+constexpr int kHalfRows = 128, kWarpRows = 32;
 constexpr int kItemRows = 2 * kHalfRows;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kSideWarp = 2, kSoftWarp = 4;
 constexpr int kThreads = 12 * 32;
@@ -66,19 +66,22 @@ constexpr uint32_t kTmemCols = 512;
 __host__ __device__ constexpr uint32_t q_bytes(int D) { return kItemRows * D * 2; }
 __host__ __device__ constexpr uint32_t kv_bytes(int D) { return kTile * D * 2; }
 // Tiles of keys and values in shared memory.
-__host__ __device__ constexpr int ring_of(int D) { return D == 128 ? 5 : 8; }
+__host__ __device__ constexpr int ring_of(int D) { return D == 128 ? 4 : 8; }
 // A value tile's clean barrier is used again 4 tiles on, its own slot 4 at most.
 static_assert(ring_of(64) <= 2 * kCleanRing && ring_of(128) <= 2 * kCleanRing, "clean ring");
+// Where a softmax warp turns its rows of 64 output elements.
+constexpr uint32_t kStageBytes = 32 * 128;
 __host__ __device__ constexpr uint32_t smem_bytes(int D) {
-  return q_bytes(D) + ring_of(D) * kv_bytes(D) + 1024;
+  return q_bytes(D) + ring_of(D) * kv_bytes(D) + 8 * kStageBytes + 1024;
 }
 
 struct PromptArgs {
-  CUtensorMap kmap, vmap, qmap;
+  CUtensorMap kmap, vmap, qmap, omap;
   int32_t kx, kz, vx, vz;  // a head's step in the maps' first and last coordinate
   const uint16_t* q;
   int64_t q_ts, q_hs;
   int32_t q_tma;  // queries are loaded by TMA: whole tokens fill a half
+  int32_t o_tma;  // outputs are stored by TMA: whole tokens fill a warp's rows
   const int32_t* q_starts;
   const int32_t* k_starts;
   int32_t max_q, max_k, window, sinks;
@@ -279,6 +282,23 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
+// A box of 64 elements from shared memory to (x, y, z), in a group of its own.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, int z,
+                                          uint32_t src) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(map),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// This thread's stores have read shared memory; have ended.
+__device__ __forceinline__ void bulk_read_wait() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // What a TMEM load has filled is not looked at before its wait.
 __device__ __forceinline__ void settle(float* s) {
 #pragma unroll
@@ -456,7 +476,8 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
       const int r = m.row0 + half * kHalfRows + rl;     // row of the sequence
       const bool live = half * kHalfRows + rl < m.rows;
       const int tok = (int)a.by_g.div(r);
-      const int64_t orow = (int64_t)(m.q0 + tok) * a.Hq + seg.head * a.G + (r - tok * a.G);
+      // (rows of the output stay below 2^31)
+      const int orow = (m.q0 + tok) * a.Hq + seg.head * a.G + (r - tok * a.G);
       // the last key that the row sees, and for the warp's first and last row
       const int pos = live ? min(m.first + tok, m.hi - 1) : -1;
       const int pos_lo = min(m.first + (int)a.by_g.div(m.row0 + w0), m.hi - 1);
@@ -550,49 +571,65 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
         const bool some = M != -INFINITY || l != l;
         const float inv = some ? __frcp_rn(l) : 0.0f;
         const float lse2 = some ? M - kShift + __log2f(l) : -INFINITY;
-        // four lanes turn their rows' 64 bytes into four times 64 bytes of a row: a
-        // store then touches 8 rows, not 32
-        int64_t to_row[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) to_row[j] = __shfl_sync(kFull, orow, (lane & ~3) + j);
-        const uint32_t lives = __ballot_sync(kFull, live) >> (lane & ~3);
+        const uint32_t stage = skv + kRing * kv_bytes(D) + (warp - kSoftWarp) * kStageBytes;
+        const uint32_t lives = __ballot_sync(kFull, live);
 #pragma unroll 1
-        for (int d = 0; d < D; d += 32) {
-          float o[32];
+        for (int d = 0; d < D; d += 64) {
+          float o[64];
           __syncwarp();
           tmem_ld32(to + d, o);
+          tmem_ld32(to + d + 32, o + 32);
           tmem_wait_ld();
           settle(o);
+          settle(o + 32);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = some ? o[j] * inv : 0.0f;
+          for (int j = 0; j < 64; j += 2) mul2(o[j], o[j + 1], o[j], o[j + 1], inv, inv);
+          if (!some)  // (0 times what an infinite value has left there)
+#pragma unroll
+            for (int j = 0; j < 64; ++j) o[j] = 0.0f;
           if (!whole) {
             if (live)
 #pragma unroll
-              for (int j = 0; j < 32; j += 4)
+              for (int j = 0; j < 64; j += 4)
                 *reinterpret_cast<float4*>(a.part_out +
                                            part_at<D>(part, d + j, half * kHalfRows + rl)) =
                     make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           } else {
-            uint32_t u[4][4];
+            // A row a lane into shared memory.  Where all of the warp's rows are there
+            // they leave by one asynchronous copy (the stores of an item's 64 KB took
+            // 2,700 cycles), else 128 bytes of a row by 8 lanes.
+            if (lane == 0) bulk_read_wait();
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) u[j / 4][j % 4] = pack16<kHalf>(o[2 * j], o[2 * j + 1]);
+            for (int j = 0; j < 8; ++j) {
+              const float* v = o + 8 * j;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                               stage + lane * 128 + ((j ^ lane) & 7) * 16),
+                           "r"(pack16<kHalf>(v[0], v[1])), "r"(pack16<kHalf>(v[2], v[3])),
+                           "r"(pack16<kHalf>(v[4], v[5])), "r"(pack16<kHalf>(v[6], v[7]))
+                           : "memory");
+            }
+            if (a.o_tma && lives == kFull) {
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) {
+                const int token = orow / a.Hq;
+                tma_store(&a.omap, d, orow - token * a.Hq, token, stage);
+              }
+            } else {
+              __syncwarp();
+              const int c = lane % 8;
 #pragma unroll
-            for (int x = 1; x < 4; x *= 2)  // lanes x apart change places
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (!(j & x))
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const bool up = (lane & x) != 0;
-                    const uint32_t got = __shfl_xor_sync(kFull, up ? u[j][e] : u[j + x][e], x);
-                    u[j][e] = up ? got : u[j][e];
-                    u[j + x][e] = up ? u[j + x][e] : got;
-                  }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (lives >> j & 1u)
-                *reinterpret_cast<uint4*>(a.out + to_row[j] * D + d + lane % 4 * 8) =
-                    make_uint4(u[j][0], u[j][1], u[j][2], u[j][3]);
+              for (int j = 0; j < 8; ++j) {
+                const int row = j * 4 + lane / 8;
+                const int at = __shfl_sync(kFull, orow, row);
+                uint32_t u[4];
+                lds128(stage + row * 128 + ((c ^ row) & 7) * 16, u);
+                if (lives >> row & 1u)
+                  *reinterpret_cast<uint4*>(a.out + (int64_t)at * D + d + c * 8) =
+                      make_uint4(u[0], u[1], u[2], u[3]);
+              }
+            }
           }
         }
         const int64_t prow = (int64_t)part * kItemRows + half * kHalfRows + rl;
@@ -605,6 +642,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
       }
       if (!more) break;
     }
+    if (lane == 0) bulk_wait();
   } else {
     set_regs_down<kOtherRegs>();
   }
@@ -1145,6 +1183,10 @@ extern "C" fp4idx_status fp4idx_prompt_attention(
   Rows qr;
   a.q_tma = query_rows(qr, q_tokens, num_heads, a.G, head_dim, q_token_stride, q_head_stride);
   if (a.q_tma && !encode(&a.qmap, q, qr, half, a.G, kHalfRows / a.G)) return FP4IDX_ERR_CUDA;
+  Rows orows;
+  a.o_tma = kWarpRows % a.G == 0 &&
+            query_rows(orows, q_tokens, num_heads, a.G, head_dim, num_heads * head_dim, head_dim);
+  if (a.o_tma && !encode(&a.omap, out, orows, half, a.G, kWarpRows / a.G)) return FP4IDX_ERR_CUDA;
   if (g_prompt_withhold.load(std::memory_order_relaxed) >= 0) {
     const int64_t held = g_prompt_withhold.exchange(-1);
     if (held < (1 << 28)) a.withhold = (int32_t)held;
