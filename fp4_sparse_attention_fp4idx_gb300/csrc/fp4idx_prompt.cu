@@ -5,6 +5,12 @@
 // What bounds it.  4 D operations per query row and key against 4 D bytes per
 // key for a whole item of 256 rows: the tensor cores and, next to them, one
 // exponential per score; for single tokens over long keys the keys' bytes.
+// Measured: 8,192 tokens, 64 heads of 128 over 8 key heads, 662 us at 1.92 GHz, 1,660
+// TFLOP/s, tensor pipe busy 74%; 16,384 tokens again and again, the clock held
+// down by the power limit, 2,740 us, 1,600 TFLOP/s (a library product of large
+// matrices sustains 1,719).  A tile of 128 keys takes a CTA 2,650 cycles, its MMAs
+// 2,048: each half's scores, softmax (1,430) and product follow one another.  32
+// single tokens over up to 20,000 keys: 140 us, 5.97 TB/s, 88% of the copy rate.
 //
 // Mathematics.  With x = softmax_scale * log2(e) * q k a row keeps M, the
 // reference of its sums, l = sum 2^(x - M + shift) and O = sum 2^(x - M + shift) v;
@@ -30,7 +36,12 @@
 //                   zero (a probability of 0 times what may lie there is NaN)
 //   warps 4-7, 8-11 softmax of half A, of half B: a row per thread, its 128
 //                   scores read from TMEM into registers, its probabilities
-//                   written back over the first half of them
+//                   written back over the first half of them, 64 keys handed to
+//                   the issuer while the other 64 are made; and the outputs, which
+//                   leave through shared memory by TMA.  (Two threads a row made a
+//                   tile 7% slower: the exponentials take as long, and each tile
+//                   has a barrier more.  A third score buffer in TMEM, which D =
+//                   64 has room for, changed nothing.)
 // TMEM: scores A and B at columns 0 and 128 (P over the first 64), O at 256 and
 // 256 + D.
 // The items and their tiles form one list, cut into equal shares, one per CTA,
@@ -137,11 +148,16 @@ __device__ __forceinline__ int key_of_tile(const Item& m, int t) {
   return (t < m.ts ? t : m.tl + (t - m.ts)) * kTile;
 }
 
-// What an item costs beside its tiles, in tiles: its queries, its first scores and
-// its output wait for one another.  Measured 8,500 cycles against 2,900 a tile (D =
-// 128); shares of equal tiles left the CTA with the shortest items 1.5 times the
-// others' time.
+// What an item costs beside its tiles, in tiles: its first scores, its last product
+// and its output wait for one another.  Measured 4,900 cycles against 2,650 a tile
+// (D = 128).  Shares of equal tiles left the CTA with the shortest items 1.5 times
+// the others' time.
 constexpr int kStart = 2;
+// Tiles up to which items are not cut.  Measured, cut against whole, us: items of up
+// to 2 tiles, one prompt of 256 tokens (32 heads over 8) 17.3 / 13.4, forty 50 / 45;
+// of 4, one of 500 19.0 / 15.8, sixty-four 138 / 133, 30 single tokens over 500 keys
+// 22.0 / 19.7; of 8, one of 1,024 25.2 / 22.0, but 4 single tokens over 1,000 keys
+// 16.5 / 23.4; of 16, one of 2,000 (8 heads over 1) 22.5 / 29.4.
 constexpr int kWhole = 4;
 
 // Where element d (a multiple of 4, and up to 3 more) of an item's row lies in
@@ -1115,7 +1131,7 @@ extern "C" fp4idx_status fp4idx_prompt_attention(
   if (!q || !q_starts || !out || !workspace || (k_tokens > 0 && (!k || !v)))
     return FP4IDX_ERR_NULL;
   if (!workspace_args_ok(batch, max_q, num_heads, kv_heads, head_dim) || max_k < 0 ||
-      q_tokens >= (1ll << 31) / num_heads || k_tokens >= (1 << 30) || max_q >= (1 << 30) ||
+      q_tokens >= (1ll << 31) / num_heads || q_tokens >= (1 << 30) || k_tokens >= (1 << 30) || max_q >= (1 << 30) ||
       max_k >= (1 << 30))
     return FP4IDX_ERR_SHAPE;
   const Rows kr = rows_of(k_tokens, kv_heads, head_dim, k_token_stride, k_head_stride);
