@@ -423,7 +423,8 @@ extern "C" fp4idx_status fp4idx_batch_extend(
   if (!free_count || (free_capacity > 0 && !free_pages) ||
       (batch > 0 && (!cached_lens || !new_lens || (block_table_pages > 0 && !block_table))))
     return FP4IDX_ERR_NULL;
-  if (context_lens && context_lens == cached_lens) return FP4IDX_ERR_ARG;
+  for (const int32_t* out : {q_starts, context_lens})
+    if (out && (out == cached_lens || out == new_lens)) return FP4IDX_ERR_ARG;
   if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) ||
       !aligned(free_pages, 4) || !aligned(free_count, 4) || !aligned(q_starts, 4) ||
       !aligned(context_lens, 4) || !aligned(slot_mapping, 8) || !aligned(positions, 8) ||

@@ -5,10 +5,10 @@
 // What bounds it.  4 D operations per query row and key against 4 D bytes per
 // key for a whole item of 256 rows: the tensor cores and, next to them, one
 // exponential per score; for single tokens over long keys the keys' bytes.
-// Measured: 8,192 tokens, 64 heads of 128 over 8 key heads, 662 us at 1.92 GHz, 1,660
-// TFLOP/s, tensor pipe busy 74%; 16,384 tokens again and again, the clock held
-// down by the power limit, 2,740 us, 1,600 TFLOP/s (a library product of large
-// matrices sustains 1,719).  A tile of 128 keys takes a CTA 2,650 cycles, its MMAs
+// Measured: 8,192 tokens, 64 heads of 128 over 8 key heads, 660 us at 1.92 GHz, 1,660
+// TFLOP/s, tensor pipe busy 74%; 16,384 tokens 2,480 to 2,750 us by how far the power
+// limit holds the clock down, 1,600 to 1,770 TFLOP/s (a library product of large
+// matrices 1,719 sustained, 1,930 in a burst).  A tile of 128 keys takes a CTA 2,650 cycles, its MMAs
 // 2,048: each half's scores, softmax (1,430) and product follow one another.  32
 // single tokens over up to 20,000 keys: 140 us, 5.97 TB/s, 88% of the copy rate.
 //

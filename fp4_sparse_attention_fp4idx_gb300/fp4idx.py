@@ -1285,7 +1285,7 @@ def rope_qk(q, k, positions, cos, sin, *, rope_style="neox", sections=None,
                 kp, kop = k.data_ptr(), k_out.data_ptr()
     _call(_lib.fp4idx_rope_qk, dev, stream, q.data_ptr(), *qs, q_out.data_ptr(), *qo, Hq, kp, *ks,
           kop, *ko, Hk, dt, D, positions.data_ptr(), st[0] if several and axes > 1 else T,
-          _sections(tuple(sections)), axes,
+          _sections(tuple(map(int, sections))), axes,
           AXES_INTERLEAVED if interleaved_axes else AXES_SECTIONS, cos.data_ptr(), sin.data_ptr(),
           max_pos, 2 * half, rope_style_code(rope_style), T, _flags(err_flags, dev))
     return q_out, k_out

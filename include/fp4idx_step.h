@@ -64,10 +64,11 @@ extern "C" {
  *                 A page belongs to one sequence where new tokens are written.
  *   free_pages    int32, a stack of free_capacity places, the lowest first.
  *   free_count    int32 [1], the pages in it; taken within [0, free_capacity].
- *   q_starts      int32 [batch+1];  context_lens int32 [batch], not the memory
- *                 of cached_lens.
+ *   q_starts      int32 [batch+1];  context_lens int32 [batch].
  *   slot_mapping, positions  int64 [num_tokens];  seq_ids, row_lens int32
- *                 [num_tokens].  Each of the six outputs may be NULL.
+ *                 [num_tokens].  Each of the six outputs may be NULL; none may lie
+ *                 in the memory of an input or of another (the lengths of the next
+ *                 step are copied from context_lens).
  * Sums of lengths stay below 2^31.  batch == 0 writes what num_tokens asks for.
  */
 fp4idx_status fp4idx_batch_extend(const int32_t* cached_lens, const int32_t* new_lens,
@@ -89,7 +90,7 @@ fp4idx_status fp4idx_batch_extend(const int32_t* cached_lens, const int32_t* new
  * share is the caller's to keep (by kept_lens) until the last one ends.
  *
  *   held_lens, kept_lens   int32 [batch]; negative counts as 0.  Pages behind
- *                 block_table_pages are not there.
+ *                 block_table_pages are not there; the others are in the table.
  *   err_flags     optional: FP4IDX_ERRFLAG_FULL if the stack has no place for a
  *                 page (it is dropped; *free_count stops at free_capacity).
  * The other arguments as above.  batch == 0 enqueues nothing.

@@ -110,6 +110,15 @@ def test_lengths_far_out_of_range():
         assert maps.context_lens.tolist()[0] == (6 if cached == [5, 9] else cached[0])
 
 
+def test_an_empty_pool_and_rows_without_pages():
+    maps, d, flags = run_extend([5, 60], [3, 4], [[1], [2]], [], 0, 9)
+    assert maps.slot_mapping.tolist() == [69, 70, 71, 188, 189, 190, 191, -1, -1] and flags == 0
+    table = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    maps = F().batch_extend(i32([0, 0]), i32([0, 1]), table, i32([]), i32([0]), 2)
+    assert maps.slot_mapping.tolist() == [-1, -1] and maps.context_lens.tolist() == [0, 0]
+    F().pages_release(i32([0, 100]), i32([0, 0]), table, i32([]), i32([0]))
+
+
 def test_no_sequences_and_no_tokens():
     maps, d, flags = run_extend([], [], [], [3, 4], 2, 5)
     assert maps.q_starts.tolist() == [0] and maps.slot_mapping.tolist() == [-1] * 5

@@ -93,6 +93,24 @@ def test_long_and_many(qs, H, Hk, D, dtype, window):
     run(qs, H, Hk, D, dtype, window=window, seed=len(qs))
 
 
+@pytest.mark.parametrize("G,Hk", [(16, 2), (32, 1), (64, 2), (128, 1), (24, 1), (100, 1)])
+@pytest.mark.parametrize("D,dtype", [(128, BF), (64, HF)])
+def test_large_groups(G, Hk, D, dtype):
+    """Up to 128 heads over one: a warp's rows, a half and an item are a few tokens or
+    part of one."""
+    run([70, 3, 1], G * Hk, Hk, D, dtype, seed=G)
+    run([5, 1], G * Hk, Hk, D, dtype, ks=[400, 2], window=90, sinks=3, seed=G)
+
+
+def test_thousands_of_sequences():
+    import random
+    r = random.Random(2)
+    qs = [r.choice([0, 1, 1, 2, 3, 40]) for _ in range(3000)]
+    run(qs, 4, 2, 64, BF, seed=1)
+    ks = [n + r.randint(0, 30) for n in qs]
+    run(qs, 4, 2, 64, BF, ks=ks, seed=2)
+
+
 @pytest.mark.parametrize("dtype,D", [(BF, 128), (HF, 64)])
 @pytest.mark.parametrize("rising", [True, False])
 def test_scores_that_rise_or_fall_along_the_keys(dtype, D, rising):

@@ -158,6 +158,17 @@ def test_offsets_beyond_32_bits():
     check(before, q.contiguous(), pos, cos, sin, [32], False, True)
 
 
+def test_one_row_of_positions_for_all_axes():
+    g = gen(8)
+    q = torch.randn(30, 2, 64, generator=g, device="cuda").to(BF)
+    cos, sin = tables(50, 32)
+    pos = torch.randint(0, 50, (30,), generator=g, device="cuda")
+    a, _ = F().rope_qk(q, None, pos, cos, sin)
+    b, _ = F().rope_qk(q, None, pos.expand(3, 30), cos, sin, sections=torch.tensor([10, 11, 11]))
+    c, none = F().rope_qk(q, q[:, :0], pos[None], cos, sin)
+    assert torch.equal(a, b) and torch.equal(a, c) and none.shape == (30, 0, 64)
+
+
 def test_strided_positions_and_another_stream():
     g = gen(7)
     T = 300

@@ -74,7 +74,9 @@ POOL = [
 @pytest.mark.fake_ptr
 @pytest.mark.parametrize("over,want", POOL + [
     (dict(T=-1), "ERR_SHAPE"), (dict(T=1 << 31), "ERR_SHAPE"), (dict(cached=None), "ERR_NULL"),
-    (dict(new=None), "ERR_NULL"), (dict(ctx=A[0]), "ERR_ARG"), (dict(cached=A[0] + 2), "ERR_ALIGN"),
+    (dict(new=None), "ERR_NULL"), (dict(ctx=A[0]), "ERR_ARG"),
+    (dict(ctx=A[1]), "ERR_ARG"), (dict(starts=A[0]), "ERR_ARG"), (dict(starts=A[1]), "ERR_ARG"),
+    (dict(cached=A[0] + 2), "ERR_ALIGN"),
     (dict(new=A[1] + 2), "ERR_ALIGN"), (dict(starts=A[5] + 2), "ERR_ALIGN"),
     (dict(ctx=A[6] + 1), "ERR_ALIGN"), (dict(slots=A[7] + 4), "ERR_ALIGN"),
     (dict(pos=A[8] + 4), "ERR_ALIGN"), (dict(ids=A[9] + 2), "ERR_ALIGN"),
