@@ -1217,14 +1217,37 @@ def _sections(sections):
     return (ctypes.c_int32 * len(sections))(*sections)
 
 
-def _out16(t, q, T, H, D, dev, name):
-    """(token stride, head stride) of an output of q's type, [T, H, D]."""
-    if t.dtype is not q.dtype:
-        raise TypeError(f"{name} must be {q.dtype}, got {t.dtype}")
-    got = _rows16(t, H, D, dev, name)
-    if len(t) != T:
-        raise ValueError(f"{name} must have T rows")
-    return got
+def _heads16(t, like, dev, name):
+    """(T, heads, D, token stride, head stride) of a 16-bit tensor on device `dev`
+    and of the type of `like`, one test for the usual case."""
+    try:
+        T, H, D = t.shape
+        ts, hs, one = t.stride()
+        if one == 1 and t.dtype is like.dtype and t.get_device() == dev and dev >= 0:
+            return T, H, D, ts if T > 1 else H * D, hs if H > 1 else D
+    except (AttributeError, ValueError):
+        pass
+    _type16(t, name)
+    _fits(t, like.dtype, 3, dev, name)
+    raise ValueError(f"{name} must be [T, heads, D] with unit element stride")
+
+
+def _tables(cos, sin, dev):
+    """(max_pos, pairs) of two dense fp32 tables."""
+    f32 = _torch().float32
+    try:
+        shape = cos.shape
+        if (cos.dtype is sin.dtype is f32 and cos.get_device() == sin.get_device() == dev and
+                sin.shape == shape and cos.is_contiguous() and sin.is_contiguous()):
+            max_pos, half = shape
+            return max_pos, half
+    except (AttributeError, ValueError):
+        pass
+    _fits(cos, f32, 2, dev, "cos")
+    _fits(sin, f32, 2, dev, "sin")
+    _dense(cos, cos.shape, "cos")
+    _dense(sin, cos.shape, "sin")
+    return cos.shape
 
 
 def rope_qk(q, k, positions, cos, sin, *, rope_style="neox", sections=None,
@@ -1237,27 +1260,16 @@ def rope_qk(q, k, positions, cos, sin, *, rope_style="neox", sections=None,
     place); outputs that are not given are allocated dense."""
     torch = _torch()
     dt = _type16(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [T, heads, D]")
     dev = q.get_device()
-    T, Hq, D = q.shape
-    qs = _rows16(q, Hq, D, dev, "q")
-    Hk, ks = 0, (0, 0)
+    T, Hq, D, *qs = _heads16(q, q, dev, "q")
+    Hk, ks, kp, kop, ko = 0, (0, 0), None, None, (0, 0)
     if k is not None:
-        if _type16(k, "k") != dt:
-            raise TypeError("q and k must have the same dtype")
-        if k.dim() != 3 or len(k) != T:
-            raise ValueError("k must be [T, heads, D] with q's tokens")
-        Hk = k.shape[1]
-        ks = _rows16(k, Hk, D, dev, "k")
+        kT, Hk, kD, *ks = _heads16(k, q, dev, "k")
+        if kT != T or kD != D:
+            raise ValueError("k must be [T, heads, D] with q's tokens and D")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _fits(cos, torch.float32, 2, dev, "cos")
-    _fits(sin, torch.float32, 2, dev, "sin")
-    shape = cos.shape
-    _dense(cos, shape, "cos")
-    _dense(sin, shape, "sin")
-    max_pos, half = shape
+    max_pos, half = _tables(cos, sin, dev)
     several = getattr(positions, "ndim", 1) == 2
     _fits(positions, torch.int64, 2 if several else 1, dev, "positions")
     st = positions.stride()
@@ -1270,25 +1282,42 @@ def rope_qk(q, k, positions, cos, sin, *, rope_style="neox", sections=None,
         sections = (half,)
     elif len(sections) != axes:
         raise ValueError("sections must have an entry for each axis of positions")
-    qo, ko, kp, kop = (Hq * D, D), (Hk * D, D), None, None
-    with _on(stream):
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-        else:
-            qo = _out16(q_out, q, T, Hq, D, dev, "q_out")
-        if k is not None:
-            if k_out is None:
-                k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device)
-            else:
-                ko = _out16(k_out, q, T, Hk, D, dev, "k_out")
-            if Hk:
-                kp, kop = k.data_ptr(), k_out.data_ptr()
+    else:
+        sections = tuple(map(int, sections))
+    if stream is None:
+        q_out, k_out, qo, ko = _rope_outputs(torch, q, k, q_out, k_out, T, Hq, Hk, D, dev)
+    else:
+        with torch.cuda.stream(stream):
+            q_out, k_out, qo, ko = _rope_outputs(torch, q, k, q_out, k_out, T, Hq, Hk, D, dev)
+    if Hk:
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     _call(_lib.fp4idx_rope_qk, dev, stream, q.data_ptr(), *qs, q_out.data_ptr(), *qo, Hq, kp, *ks,
-          kop, *ko, Hk, dt, D, positions.data_ptr(), st[0] if several and axes > 1 else T,
-          _sections(tuple(map(int, sections))), axes,
-          AXES_INTERLEAVED if interleaved_axes else AXES_SECTIONS, cos.data_ptr(), sin.data_ptr(),
-          max_pos, 2 * half, rope_style_code(rope_style), T, _flags(err_flags, dev))
+          kop, *ko, Hk, dt, D, positions.data_ptr(), st[0] if axes > 1 else T,
+          _sections(sections), axes, AXES_INTERLEAVED if interleaved_axes else AXES_SECTIONS,
+          cos.data_ptr(), sin.data_ptr(), max_pos, 2 * half, rope_style_code(rope_style), T,
+          None if err_flags is None else _flags(err_flags, dev))
     return q_out, k_out
+
+
+def _rope_outputs(torch, q, k, q_out, k_out, T, Hq, Hk, D, dev):
+    """Outputs, made where not given, and their strides."""
+    qo, ko = (Hq * D, D), (Hk * D, D)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    else:
+        *shape, a, b = _heads16(q_out, q, dev, "q_out")
+        if shape != [T, Hq, D]:
+            raise ValueError("q_out must have q's shape")
+        qo = a, b
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device)
+        else:
+            *shape, a, b = _heads16(k_out, q, dev, "k_out")
+            if shape != [T, Hk, D]:
+                raise ValueError("k_out must have k's shape")
+            ko = a, b
+    return q_out, k_out, qo, ko
 
 
 def prompt_workspace_bytes(batch: int, max_q: int, num_heads: int, kv_heads: int,
@@ -1314,20 +1343,16 @@ def prompt_attention(q, k, v, q_starts, max_q: int, *, k_starts=None, max_k=None
     to D^-1/2.  Rows of out and lse in no sequence are left as they were."""
     torch = _torch()
     dt = _type16(q, "q")
-    if _type16(k, "k") != dt or _type16(v, "v") != dt:
-        raise TypeError("q, k and v must have the same dtype")
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q must be [Tq, H, D], k and v [Tk, kv_heads, D]")
     dev = q.get_device()
-    (Tq, H, D), (Tk, Hk, _) = q.shape, k.shape
-    qs, ks, vs = _rows16(q, H, D, dev, "q"), _rows16(k, Hk, D, dev, "k"), \
-        _rows16(v, Hk, D, dev, "v")
-    if v.shape[0] != Tk:
-        raise ValueError("k and v must have the same tokens")
+    Tq, H, D, *qs = _heads16(q, q, dev, "q")
+    Tk, Hk, kD, *ks = _heads16(k, q, dev, "k")
+    vT, vH, vD, *vs = _heads16(v, q, dev, "v")
+    if vT != Tk or vH != Hk or vD != D or kD != D:
+        raise ValueError("k and v must have the same tokens and heads, and q's D")
     if Hk == 0 or H % Hk:
         raise ValueError("q's heads must be a multiple of k's")
     _fits(q_starts, torch.int32, 1, dev, "q_starts")
-    batch = q_starts.shape[0] - 1
+    batch = len(q_starts) - 1
     if batch < 0 or not q_starts.is_contiguous():
         raise ValueError("q_starts must be contiguous [batch+1]")
     kst = None
@@ -1341,26 +1366,28 @@ def prompt_attention(q, k, v, q_starts, max_q: int, *, k_starts=None, max_k=None
         raise ValueError("without k_starts, q and k must have the same tokens")
     if max_k is None:
         max_k = max_q
-    with _on(stream):
-        if out is None:
-            out = torch.empty((Tq, H, D), dtype=q.dtype, device=q.device)
-        else:
-            _fits(out, q.dtype, 3, dev, "out")
-            _dense(out, (Tq, H, D), "out")
-        if lse is None:
-            lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
-        else:
-            _fits(lse, torch.float32, 2, dev, "lse")
-            _dense(lse, (Tq, H), "lse")
-        if workspace is None:
-            workspace = torch.empty(_prompt_workspace(batch, max_q, H, Hk, D), dtype=torch.uint8,
-                                    device=q.device)
-        else:
-            _fits(workspace, torch.uint8, 1, dev, "workspace")
-            _dense(workspace, workspace.shape, "workspace")
+    if out is not None:
+        _fits(out, q.dtype, 3, dev, "out")
+        _dense(out, (Tq, H, D), "out")
+    if lse is not None:
+        _fits(lse, torch.float32, 2, dev, "lse")
+        _dense(lse, (Tq, H), "lse")
+    if workspace is not None:
+        _fits(workspace, torch.uint8, 1, dev, "workspace")
+        _dense(workspace, workspace.shape, "workspace")
+    if out is None or lse is None or workspace is None:
+        with _on(stream):
+            at = q.device
+            if out is None:
+                out = torch.empty((Tq, H, D), dtype=q.dtype, device=at)
+            if lse is None:
+                lse = torch.empty((Tq, H), dtype=torch.float32, device=at)
+            if workspace is None:
+                workspace = torch.empty(_prompt_workspace(batch, max_q, H, Hk, D),
+                                        dtype=torch.uint8, device=at)
     _call(_lib.fp4idx_prompt_attention, dev, stream, q.data_ptr(), *qs, k.data_ptr(), *ks,
           v.data_ptr(), *vs, dt, q_starts.data_ptr(), kst, max_q, max_k, window, sinks,
           D ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), lse.data_ptr(),
           batch, Tq, Tk, H, Hk, D, workspace.data_ptr(), workspace.numel(),
-          _flags(err_flags, dev))
+          None if err_flags is None else _flags(err_flags, dev))
     return out, lse
