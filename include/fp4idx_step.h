@@ -177,7 +177,8 @@ fp4idx_status fp4idx_rope_qk(const void* q, int64_t q_token_stride, int64_t q_he
  *   max_q         a bound on n_b; tokens of a sequence behind its max_q-th are
  *                 left unwritten.
  *   max_k         a bound on c_b; keys behind a sequence's max_k-th are not
- *                 seen.
+ *                 seen.  The work split is chosen by both bounds, so loose ones
+ *                 cost time, not correctness.
  *   softmax_scale not negative.
  *   head_dim      64 or 128;  kv_heads 1 .. 65535, num_heads a multiple of it.
  *   out           16-bit [q_tokens, num_heads, head_dim], dense, 16-byte
