@@ -8,9 +8,10 @@
 // Measured: 8,192 tokens, 64 heads of 128 over 8 key heads, 660 us at 1.92 GHz, 1,660
 // TFLOP/s, tensor pipe busy 74%; 16,384 tokens 2,480 to 2,750 us by how far the power
 // limit holds the clock down, 1,600 to 1,770 TFLOP/s (a library product of large
-// matrices 1,719 sustained, 1,930 in a burst).  A tile of 128 keys takes a CTA 2,650 cycles, its MMAs
-// 2,048: each half's scores, softmax (1,430) and product follow one another.  32
-// single tokens over up to 20,000 keys: 140 us, 5.97 TB/s, 88% of the copy rate.
+// matrices 1,719 sustained, 1,930 in a burst).  A tile of 128 keys takes a CTA 2,650
+// cycles, its MMAs 2,048: each half's scores, softmax (1,430) and product follow one
+// another.  32 single tokens over up to 20,000 keys: 140 us, 5.97 TB/s, 88% of the
+// copy rate.
 //
 // Mathematics.  With x = softmax_scale * log2(e) * q k a row keeps M, the
 // reference of its sums, l = sum 2^(x - M + shift) and O = sum 2^(x - M + shift) v;
@@ -758,7 +759,8 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
     // ---------------------------------------------------------- MMA issuer
     constexpr uint32_t kQkDesc = idesc16(kTile, kHalf, false), kPvDesc = idesc16(D, kHalf, true);
     // a descriptor's address field moves by (bytes >> 4)
-    const uint64_t dq = sw128_desc(sq), dk = sw128_desc(skv), dv = sw128_rows_desc(skv, D == 128 ? kBlock : 1024);
+    const uint64_t dq = sw128_desc(sq), dk = sw128_desc(skv);
+    const uint64_t dv = sw128_rows_desc(skv, D == 128 ? kBlock : 1024);
     const uint32_t elected = elect_one();
     const auto issue_s = [&](int half, uint32_t slot) {
       const uint64_t qa = dq + half * (kBlocks * kBlock >> 4);
@@ -1144,8 +1146,8 @@ extern "C" fp4idx_status fp4idx_prompt_attention(
   if (!q || !q_starts || !out || !workspace || (k_tokens > 0 && (!k || !v)))
     return FP4IDX_ERR_NULL;
   if (!workspace_args_ok(batch, max_q, num_heads, kv_heads, head_dim) || max_k < 0 ||
-      q_tokens >= (1ll << 31) / num_heads || q_tokens >= (1 << 30) || k_tokens >= (1 << 30) || max_q >= (1 << 30) ||
-      max_k >= (1 << 30))
+      q_tokens >= (1ll << 31) / num_heads || q_tokens >= (1 << 30) || k_tokens >= (1 << 30) ||
+      max_q >= (1 << 30) || max_k >= (1 << 30))
     return FP4IDX_ERR_SHAPE;
   const Rows kr = rows_of(k_tokens, kv_heads, head_dim, k_token_stride, k_head_stride);
   const Rows vr = rows_of(k_tokens, kv_heads, head_dim, v_token_stride, v_head_stride);
@@ -1169,8 +1171,9 @@ extern "C" fp4idx_status fp4idx_prompt_attention(
   a.k_starts = k_starts ? k_starts : q_starts;
   a.max_q = (int32_t)max_q;
   a.max_k = (int32_t)max_k;
-  // a window that holds every key is no window
-  a.window = window < max_k ? (int32_t)window : 0;
+  // a window that holds every key is no window (a sequence may have more than max_k:
+  // its window still ends at the query)
+  a.window = window < k_tokens ? (int32_t)window : 0;
   a.sinks = (int32_t)(sinks < max_k ? sinks : max_k);
   a.batch = (int32_t)batch;
   a.Tq = (int32_t)q_tokens;

@@ -218,6 +218,18 @@ def test_tokens_behind_max_q_are_left_unwritten():
         assert bool((out[max_q:] == 3).all()) and bool((lse[max_q:] == 3).all())
 
 
+@pytest.mark.parametrize("max_k", [1, 100, 128, 300, 599])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 3), (100, 0), (300, 40), (400, 0), (600, 0)])
+def test_keys_behind_max_k_are_not_seen(max_k, window, sinks):
+    """A window ends at the query, which may stand behind the last key that counts."""
+    qs, ks = [130, 2], [600, 90]
+    q, k, v = inputs(qs, ks, 4, 2, 64, BF, max_k + window)
+    ref = R.attend(q, k, v, prefix(qs), prefix(ks), window, sinks, 64 ** -0.5, max_k=max_k)
+    out, lse = F().prompt_attention(q, k, v, i32(prefix(qs)), 130, k_starts=i32(prefix(ks)),
+                                    max_k=max_k, window=window, sinks=sinks)
+    R.check(out, lse, ref)
+
+
 @pytest.mark.parametrize("D,dtype", [(128, BF), (64, HF)])
 @pytest.mark.parametrize("H,Hk", [(8, 2), (6, 2), (3, 3)])
 def test_layouts(D, dtype, H, Hk):
