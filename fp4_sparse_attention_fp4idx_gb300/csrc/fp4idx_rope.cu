@@ -183,6 +183,16 @@ extern "C" fp4idx_status fp4idx_rope_qk(
       (rope_style != FP4IDX_ROPE_NEOX && rope_style != FP4IDX_ROPE_INTERLEAVED) ||
       (axis_order != FP4IDX_AXES_SECTIONS && axis_order != FP4IDX_AXES_INTERLEAVED))
     return FP4IDX_ERR_ARG;
+  // in place is row by row
+  const auto moves = [&](const void* in, const void* out, int64_t heads, int64_t ts, int64_t hs,
+                         int64_t ots, int64_t ohs) {
+    return in == out && ((num_tokens > 1 && ts != ots) || (heads > 1 && hs != ohs));
+  };
+  if (moves(q, q_out, q_heads, q_token_stride, q_head_stride, q_out_token_stride,
+            q_out_head_stride) ||
+      (k_heads > 0 && moves(k, k_out, k_heads, k_token_stride, k_head_stride, k_out_token_stride,
+                            k_out_head_stride)))
+    return FP4IDX_ERR_ARG;
   const int half = (int)(rope_dim / 2);
   int64_t sum = 0;
   for (int x = 0; x < num_axes; ++x) {

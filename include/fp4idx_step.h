@@ -122,8 +122,9 @@ enum {
  *                 16-byte aligned, strides multiples of 8.  k may be NULL with
  *                 k_heads 0.
  *   q_out, k_out  the same, with strides of their own.  q_out may be q with q's
- *                 strides (in place), and k_out k; any other overlap of an
- *                 output with an input is the caller's error.
+ *                 strides (in place; other strides return FP4IDX_ERR_ARG), and
+ *                 k_out k; any other overlap of an output with an input is the
+ *                 caller's error.
  *   q_heads       at least 1; q_heads + k_heads at most 65535.
  *   head_dim      a multiple of 8, 16 .. 1024;  rope_dim a multiple of 16, at
  *                 most head_dim.
@@ -183,7 +184,7 @@ fp4idx_status fp4idx_rope_qk(const void* q, int64_t q_token_stride, int64_t q_he
  *   head_dim      64 or 128;  kv_heads 1 .. 65535, num_heads a multiple of it.
  *   out           16-bit [q_tokens, num_heads, head_dim], dense, 16-byte
  *                 aligned;  lse optional fp32 [q_tokens, num_heads], natural
- *                 logarithm.
+ *                 logarithm.  Neither lies in the memory of an input.
  *   workspace     fp4idx_prompt_workspace_bytes(batch, max_q, num_heads,
  *                 kv_heads, head_dim) bytes (0 bytes: arguments out of range),
  *                 16-byte aligned, contents not kept; its own for each call in

@@ -136,6 +136,14 @@ def test_rope_refusals(F, over, want):
     assert call_rope(F, over) == getattr(F, want)
 
 
+@pytest.mark.fake_ptr
+@pytest.mark.parametrize("over", [
+    dict(qo=A[0], qots=2048), dict(qo=A[0], qohs=640), dict(ko=A[2], kots=512),
+    dict(ko=A[2], kohs=640), dict(qo=A[0], qots=2048, T=5, k=None, Hk=0)], ids=str)
+def test_rope_in_place_with_other_strides_is_refused(F, over):
+    assert call_rope(F, over) == F.ERR_ARG
+
+
 def call_prompt(F, over):
     a = dict(q=A[0], qts=1024, qhs=128, k=A[1], kts=256, khs=128, v=A[2], vts=256, vhs=128, dt=0,
              qs=A[3], ks=None, max_q=9, max_k=9, window=0, sinks=0, scale=0.1, out=A[4], lse=A[5],
