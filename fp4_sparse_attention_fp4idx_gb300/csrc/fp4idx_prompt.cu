@@ -81,6 +81,8 @@ __host__ __device__ constexpr uint32_t kv_bytes(int D) { return kTile * D * 2; }
 __host__ __device__ constexpr int ring_of(int D) { return D == 128 ? 4 : 8; }
 // A value tile's clean barrier is used again 4 tiles on, its own slot 4 at most.
 static_assert(ring_of(64) <= 2 * kCleanRing && ring_of(128) <= 2 * kCleanRing, "clean ring");
+// Keys and values take turns, so that values have the odd slots to themselves.
+static_assert(ring_of(64) % 2 == 0 && ring_of(128) % 2 == 0, "a slot holds keys or values");
 // Where a softmax warp turns its rows of 64 output elements.
 constexpr uint32_t kStageBytes = 32 * 128;
 __host__ __device__ constexpr uint32_t smem_bytes(int D) {
@@ -724,10 +726,11 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
         }
       }
       for (int t = seg.t0; t < seg.t1 && ok; ++t, ++n) {
-        // (the keys' phase too: a wait that skips one takes the next for it)
-        const uint32_t uk = 2 * n, u = uk + 1;
-        ok = wait(B::kFullAt + uk % kRing, uk / kRing & 1u) &&
-             wait(B::kFullAt + u % kRing, u / kRing & 1u);
+        // (the value tile alone, whose slot is not filled again before this warp's
+        // arrival: a key tile's slot is given back without it, so that its barrier
+        // could complete twice unseen)
+        const uint32_t u = 2 * n + 1;
+        ok = wait(B::kFullAt + u % kRing, u / kRing & 1u);
         if (!ok) break;
         const int kb = key_of_tile(m, t);
         // this warp's 64 rows of the tile
