@@ -14,14 +14,18 @@
 // copy rate.
 //
 // Mathematics.  With x = softmax_scale * log2(e) * q k a row keeps M, the
-// reference of its sums, l = sum 2^(x - M + shift) and O = sum 2^(x - M + shift) v;
-// out = O / l.  M follows the largest x only when that has grown by more than
-// kSlack, so the sums in TMEM are seldom rescaled.  Probabilities are rounded to
-// the elements' type for the product with the values (the tensor core wants both
-// operands of one type): bf16 keeps fp32's range, and 2^8 is as far as one may
-// exceed M; in fp16 they are shifted up by 2^10 and may grow by 2^4 more, so that
-// the smallest that does not vanish is 2^-35 of the largest.  l is summed from
-// the unrounded ones.
+// reference of its sums, l = sum 2^(x - M) and O = sum 2^(x - M) v; out = O / l.
+// M is kShift below an x that was the row's largest, and follows the largest only
+// when that has grown by more than kSlack, so the sums in TMEM are seldom rescaled.
+// Probabilities 2^(x - M) are rounded to the elements' type for the product with the
+// values (the tensor core wants both operands of one type); l is summed from the
+// unrounded ones.  bf16 has fp32's range: one may grow to 2^8, all are shifted down
+// by 2^6, so that O is in range where sum 2^(x - top) |v| < 2^125, top the row's
+// largest x, and that none above 2^-120 of the largest vanishes.  (A slack of 2^4,
+// which needs less of a shift, takes up to 10% more time: 8,192 tokens, 32 heads of
+// 128 over 8, scores of standard deviation 2, 344 -> 378 us.)  In fp16 they are shifted
+// up by 2^10 and may grow by 2^4 more, and the smallest that does not vanish is 2^-35
+// of the largest.
 //
 // Roles (one CTA per SM).  An item is 256 rows (token i, head g of a key head's
 // group: row i * G + g) of a sequence, as two M = 128 halves A and B that share
@@ -428,7 +432,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
   constexpr int kBlocks = D / 64;               // 64-element column blocks of a row
   constexpr uint32_t kBlock = kTile * 128;      // bytes of one, of 128 rows
   constexpr int kRing = ring_of(D);
-  constexpr float kShift = kHalf ? 10.0f : 0.0f, kSlack = kHalf ? 4.0f : 8.0f;
+  constexpr float kShift = kHalf ? 10.0f : -6.0f, kSlack = kHalf ? 4.0f : 8.0f;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl<D> ctl;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -557,10 +561,10 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
           };
           const float x = top();
           // ---- the sums' reference, moved seldom
-          const bool move = x > M + kSlack || (M == -INFINITY && x != -INFINITY);
+          const bool move = x > M + (kShift + kSlack) || (M == -INFINITY && x != -INFINITY);
           if (__builtin_expect(__any_sync(kFull, move), 0)) {
-            const float al = move ? exp2_approx(M - x) : 1.0f;
-            if (move) M = x;
+            const float al = move ? exp2_approx(M - (x - kShift)) : 1.0f;
+            if (move) M = x - kShift;
             l *= al;
             if (t > 0) {
               // few columns at a time: s stays in registers
@@ -579,12 +583,12 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
             }
           }
           float sum = 0.0f;
-          probabilities<kHalf>(s, c, or_zero(M) - kShift, ts, sum);
+          probabilities<kHalf>(s, c, or_zero(M), ts, sum);
           tmem_wait_st();
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B::kPHalf + half));
-          probabilities<kHalf>(s + 64, c, or_zero(M) - kShift, ts + 32, sum);
+          probabilities<kHalf>(s + 64, c, or_zero(M), ts + 32, sum);
           l += sum;
           tmem_wait_st();
         } else if (lane == 0) {
@@ -602,7 +606,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
         // (scores that are all NaN move no reference)
         const bool some = M != -INFINITY || l != l;
         const float inv = some ? __frcp_rn(l) : 0.0f;
-        const float lse2 = some ? M - kShift + __log2f(l) : -INFINITY;
+        const float lse2 = some ? M + __log2f(l) : -INFINITY;
         const uint32_t stage = skv + kRing * kv_bytes(D) + (warp - kSoftWarp) * kStageBytes;
         const uint32_t lives = __ballot_sync(kFull, live);
 #pragma unroll 1

@@ -161,9 +161,11 @@ fp4idx_status fp4idx_rope_qk(const void* q, int64_t q_token_stride, int64_t q_he
  *
  * Products are exact in the tensor core, the softmax and both sums fp32;
  * probabilities are rounded to the elements' type before the product with the
- * values: bf16 by 2^-8 of themselves, fp16 by 2^-11 or 2^-35 of the row's
- * largest.  A score carries fp32's relative error into its exponent, so |x_s| is
- * to stay below 2^20.
+ * values: bf16 by 2^-8 of themselves (those below 2^-120 of the row's largest count
+ * as 0), fp16 by 2^-11 or 2^-35 of the row's largest.  A score carries fp32's
+ * relative error into its exponent, so |x_s| is to stay below 2^20.  The sum over
+ * the keys of exp(x_s - max x) |v_s[d]| is to stay below 2^125, as it does for values
+ * below 2^125 divided by the keys; beyond it an output may be infinite.
  *
  *   q             16-bit, row (t, h) at t*q_token_stride + h*q_head_stride
  *                 elements; 16-byte aligned, strides multiples of 8.
