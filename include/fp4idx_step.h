@@ -132,6 +132,9 @@ enum {
  *   sections      HOST int32 [num_axes], not negative, their sum R / 2; read
  *                 within the call.  num_axes 1 .. 4.
  *   cos, sin      fp32 [max_pos, R / 2] each, dense, 16-byte aligned.
+ *   num_tokens    below 2^31, and num_tokens * ceil(head_dim / 16) * ceil((q_heads +
+ *                 k_heads) / 8) below 2^32 - 256, as many threads as a call has;
+ *                 more return FP4IDX_ERR_SHAPE and take several calls.
  *   err_flags     optional: FP4IDX_ERRFLAG_POSITION for a token with a position
  *                 outside [0, max_pos); its rows are left as they were.
  * num_tokens == 0 returns FP4IDX_OK and enqueues nothing.
