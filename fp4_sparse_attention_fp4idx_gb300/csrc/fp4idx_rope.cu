@@ -12,6 +12,8 @@
 // take a head's units, then the next head's, so that a warp reads a run of memory.
 // Which axis turns a pair is two bits of a table made on the host.
 
+#include <utility>
+
 #include "fp4idx_attn.cuh"
 #include "fp4idx_step.h"
 
@@ -200,10 +202,25 @@ extern "C" fp4idx_status fp4idx_rope_qk(
     sum += sections[x];
   }
   if (sum != half) return FP4IDX_ERR_ARG;
-  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(k_out, 16) ||
-      q_token_stride % 8 || q_head_stride % 8 || q_out_token_stride % 8 || q_out_head_stride % 8 ||
+  if (q_token_stride % 8 || q_head_stride % 8 || q_out_token_stride % 8 || q_out_head_stride % 8 ||
       (k_heads > 0 && (k_token_stride % 8 || k_head_stride % 8 || k_out_token_stride % 8 ||
-                       k_out_head_stride % 8)) ||
+                       k_out_head_stride % 8)))
+    return FP4IDX_ERR_ALIGN;
+  // two threads would write one row of an output
+  const auto overlap = [&](int64_t heads, int64_t ts, int64_t hs) {
+    int64_t near = ts < 0 ? -ts : ts, far = hs < 0 ? -hs : hs, n = num_tokens;
+    if (heads == 1) return num_tokens > 1 && near < head_dim;
+    if (num_tokens == 1) return far < head_dim;
+    if (near > far) {
+      std::swap(near, far);
+      n = heads;
+    }
+    return near < head_dim || far < head_dim || (n - 1) > (far - head_dim) / near;
+  };
+  if (overlap(q_heads, q_out_token_stride, q_out_head_stride) ||
+      (k_heads > 0 && overlap(k_heads, k_out_token_stride, k_out_head_stride)))
+    return FP4IDX_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(k_out, 16) ||
       !aligned(positions, 8) || !aligned(cos, 16) || !aligned(sin, 16) || !aligned(err_flags, 4))
     return FP4IDX_ERR_ALIGN;
   RopeArgs a = {};

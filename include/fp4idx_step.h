@@ -121,7 +121,9 @@ enum {
  *   q, k          16-bit, row (t, h) at t*token_stride + h*head_stride elements,
  *                 16-byte aligned, strides multiples of 8.  k may be NULL with
  *                 k_heads 0.
- *   q_out, k_out  the same, with strides of their own.  q_out may be q with q's
+ *   q_out, k_out  the same, with strides of their own; an output's heads lie within
+ *                 its token stride or a head's tokens within its head stride, so that
+ *                 no two rows overlap (FP4IDX_ERR_ARG).  q_out may be q with q's
  *                 strides (in place; other strides return FP4IDX_ERR_ARG), and
  *                 k_out k; any other overlap of an output with an input is the
  *                 caller's error.

@@ -39,3 +39,25 @@ def test_rope_of_more_threads_than_a_grid_counts_is_refused(F, T, H, Hk, D, R):
                                qots=H * D, qohs=D, **k)) == F.ERR_SHAPE
     assert "num_tokens * ceil(head_dim / 16) * ceil((q_heads + k_heads) / 8) below 2^32 - 256" \
         in header(F)
+
+
+@pytest.mark.parametrize("over", [
+    # a broadcast tensor in place, or as an output: over the heads, over the tokens
+    dict(q=A.A[0], qo=A.A[0], qts=128, qhs=0, qots=128, qohs=0), dict(qots=1024, qohs=0),
+    dict(qots=0, qohs=128), dict(ko=A.A[2], kts=128, khs=0, kots=128, kohs=0),
+    dict(kots=0, kohs=128),
+    # rows, tokens or heads that reach into the next ones
+    dict(qohs=120), dict(qots=128, qohs=128), dict(qots=1016), dict(qots=-1016, qohs=128),
+    dict(qots=128, qohs=4 * 128 + 120), dict(H=1, qots=120), dict(T=1, qohs=64),
+    dict(Hk=1, kots=64, kohs=128), dict(kots=256, kohs=-120)], ids=str)
+def test_rope_outputs_whose_rows_overlap_are_refused(F, over):
+    assert A.call_rope(F, over) == F.ERR_ARG
+
+
+@pytest.mark.parametrize("over", [
+    # an error behind that check shows that it lets these through
+    dict(qots=128, qohs=5 * 128), dict(qots=-1024, qohs=128), dict(qots=1024, qohs=-128),
+    dict(T=1, qots=0), dict(H=1, qohs=0), dict(kots=1024, kohs=136), dict(qots=136, qohs=8 * 136),
+    dict(Hk=1, kohs=0, kots=128)], ids=str)
+def test_rope_outputs_whose_rows_do_not_overlap_are_not(F, over):
+    assert A.call_rope(F, dict(over, pos=A.A[4] + 4)) == F.ERR_ALIGN
