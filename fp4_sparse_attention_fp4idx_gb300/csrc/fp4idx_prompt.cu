@@ -1040,6 +1040,21 @@ bool workspace_args_ok(int64_t batch, int64_t max_q, int64_t num_heads, int64_t 
          max_q < (1ll << 31) / num_heads;
 }
 
+// CTAs of a call: one per SM, or as many as its items can have tiles, where a key head
+// has `rows` rows in all.
+constexpr int grid_of(int64_t rows, int64_t batch, int64_t kv_heads, int64_t max_k) {
+  const int64_t chunks = (rows + kItemRows - 1) / kItemRows + batch;
+  if (chunks >= kMaxGrid) return kMaxGrid;
+  const int64_t tiles = chunks * kv_heads * (max_k / kTile + 1);  // below 2^47
+  return tiles < kMaxGrid ? (int)tiles : (int)kMaxGrid;
+}
+static_assert(grid_of(1, 1, 1, 0) == 2 && grid_of(256, 1, 2, 1000) == 32, "tiles of a small call");
+// (the largest sizes that a call may have: the product of all does not fit 64 bits)
+static_assert(grid_of((1ll << 31) - 1, (1ll << 31) - 1, 65535, (1 << 30) - 1) == kMaxGrid &&
+                  grid_of(1, 1, 65535, (1 << 30) - 1) == kMaxGrid &&
+                  grid_of(1, kMaxGrid - 2, 65535, (1 << 30) - 1) == kMaxGrid,
+              "tiles of the largest calls");
+
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
 
 // The driver's call that describes a tensor to the TMA unit.
@@ -1230,10 +1245,7 @@ extern "C" fp4idx_status fp4idx_prompt_attention(
     const int64_t held = g_prompt_withhold.exchange(-1);
     if (held < (1 << 28)) a.withhold = (int32_t)held;
   }
-  // (at most 2^31 items of at most 2^23 tiles)
-  const int64_t items = ((q_tokens * a.G + kItemRows - 1) / kItemRows + batch) * kv_heads;
-  const int64_t units = items * (max_k / kTile + 1);
-  const int grid = units < kMaxGrid ? (int)units : kMaxGrid;
+  const int grid = grid_of(q_tokens * a.G, batch, kv_heads, max_k);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (head_dim == 128)
     return half ? launch_prompt<128, true>(a, grid, s) : launch_prompt<128, false>(a, grid, s);
