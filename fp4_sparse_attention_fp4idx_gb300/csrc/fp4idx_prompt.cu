@@ -1177,7 +1177,7 @@ extern "C" fp4idx_status fp4idx_prompt_attention(
   const Workspace w = workspace_of(head_dim);
   if (workspace_bytes < (size_t)w.total) return FP4IDX_ERR_SCRATCH;
   if (!dtype_ok(dtype) || !isfinite(softmax_scale) || softmax_scale < 0.0f || window < 0 ||
-      sinks < 0)
+      sinks < 0 || out == q || (k_tokens > 0 && (out == k || out == v)))
     return FP4IDX_ERR_ARG;
   if (!aligned(q, 16) || q_token_stride % 8 || q_head_stride % 8 || !aligned(k, 16) ||
       !aligned(v, 16) || (k_tokens > 0 && (!kr.align_ok || !vr.align_ok)) || !aligned(out, 16) ||

@@ -191,7 +191,8 @@ fp4idx_status fp4idx_rope_qk(const void* q, int64_t q_token_stride, int64_t q_he
  *   head_dim      64 or 128;  kv_heads 1 .. 65535, num_heads a multiple of it.
  *   out           16-bit [q_tokens, num_heads, head_dim], dense, 16-byte
  *                 aligned;  lse optional fp32 [q_tokens, num_heads], natural
- *                 logarithm.  Neither lies in the memory of an input.
+ *                 logarithm.  Neither lies in the memory of an input (out where q,
+ *                 k or v begins: FP4IDX_ERR_ARG).
  *   workspace     fp4idx_prompt_workspace_bytes(batch, max_q, num_heads,
  *                 kv_heads, head_dim) bytes (0 bytes: arguments out of range),
  *                 16-byte aligned, contents not kept; its own for each call in

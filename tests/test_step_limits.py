@@ -61,3 +61,10 @@ def test_rope_outputs_whose_rows_overlap_are_refused(F, over):
     dict(Hk=1, kohs=0, kots=128)], ids=str)
 def test_rope_outputs_whose_rows_do_not_overlap_are_not(F, over):
     assert A.call_rope(F, dict(over, pos=A.A[4] + 4)) == F.ERR_ALIGN
+
+
+@pytest.mark.parametrize("over", [
+    dict(out=A.A[0]), dict(out=A.A[1]), dict(out=A.A[2]), dict(out=A.A[0], H=2, qts=256)], ids=str)
+def test_prompt_output_in_place_of_an_input_is_refused(F, over):
+    """Other work of the call reads rows after they are written."""
+    assert A.call_prompt(F, dict(over, qs=A.A[3] + 2)) == F.ERR_ARG
