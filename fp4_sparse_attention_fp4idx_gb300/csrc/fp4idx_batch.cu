@@ -5,7 +5,10 @@
 // for each 64), 8 to 20 read and written for each sequence: for a decode step
 // nothing but latency, so everything is one launch.  Both calls are a running
 // sum over the sequences and then, for every token (every page), the search for
-// its sequence in those sums.
+// its sequence in those sums.  Measured, an extension in a captured graph: 7
+// sequences by 4 tokens 3.4 us, 2.6 of it the launch; 3,000 by 2 tokens 10.9 (sums 3.3,
+// search and maps 5.0); 256 by 230 tokens 13.2 (sums 0.7, 1.4 MB written 5.2, search
+// and maps 4.7).
 //
 // Layout.  One cluster of 1 or 8 CTAs.  Every CTA makes the running sums of all
 // sequences, four to a thread and 4,096 at a time in shared memory, and the

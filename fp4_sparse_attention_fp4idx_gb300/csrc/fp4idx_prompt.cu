@@ -5,13 +5,13 @@
 // What bounds it.  4 D operations per query row and key against 4 D bytes per
 // key for a whole item of 256 rows: the tensor cores and, next to them, one
 // exponential per score; for single tokens over long keys the keys' bytes.
-// Measured: 8,192 tokens, 64 heads of 128 over 8 key heads, 660 us at 1.92 GHz, 1,660
-// TFLOP/s, tensor pipe busy 74%; 16,384 tokens 2,480 to 2,750 us by how far the power
-// limit holds the clock down, 1,600 to 1,770 TFLOP/s (a library product of large
-// matrices 1,719 sustained, 1,930 in a burst).  A tile of 128 keys takes a CTA 2,650
-// cycles, its MMAs 2,048: each half's scores, softmax (1,430) and product follow one
-// another.  32 single tokens over up to 20,000 keys: 140 us, 5.97 TB/s, 88% of the
-// copy rate.
+// Measured: 8,192 tokens, 64 heads of 128 over 8 key heads, 660 to 670 us at 1.92 GHz,
+// 1,640 to 1,660 TFLOP/s, tensor pipe busy 74%, and 712 us (1.83 GHz) call after call;
+// 16,384 tokens 2,480 us (1.9 GHz) to 2,810 us (1.72 GHz) by how far the power limit
+// holds the clock down, 1,560 to 1,770 TFLOP/s (a library product of large matrices
+// 1,719 sustained, 1,930 in a burst).  A tile of 128 keys takes a CTA 2,570 cycles, its
+// MMAs 2,048: each half's scores, softmax (1,430) and product follow one another.  32
+// single tokens over up to 20,000 keys: 140 us, 5.97 TB/s, 88% of the copy rate.
 //
 // Mathematics.  With x = softmax_scale * log2(e) * q k a row keeps M, the
 // reference of its sums, l = sum 2^(x - M) and O = sum 2^(x - M) v; out = O / l.
@@ -156,9 +156,10 @@ __device__ __forceinline__ int key_of_tile(const Item& m, int t) {
 }
 
 // What an item costs beside its tiles, in tiles: its first scores, its last product
-// and its output wait for one another.  Measured 4,900 cycles against 2,650 a tile
-// (D = 128).  Shares of equal tiles left the CTA with the shortest items 1.5 times
-// the others' time.
+// and its output wait for one another.  Measured (fitted to 1 to 4 items a CTA of 2 to
+// 32 tiles) 5,400 cycles against 2,570 a tile for D = 128, 4,200 against 2,240 for D =
+// 64.  Shares of equal tiles left the CTA with the shortest items 1.5 times the
+// others' time.
 constexpr int kStart = 2;
 // Tiles up to which items are not cut.  Measured, cut against whole, us: items of up
 // to 2 tiles, one prompt of 256 tokens (32 heads over 8) 17.3 / 13.4, forty 50 / 45;
@@ -470,8 +471,6 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
   fence_after();
   const uint32_t tmem = __shfl_sync(kFull, ctl.tmem, 0);
   const uint32_t bars = bar(0);
-  // (a first look without a loop: its code costs a hundred cycles on the issuer's
-  // path from one half's softmax to its products)
   const auto wait = [&](int i, uint32_t parity) {
     const uint32_t b = bars + i * 8;
     return wait_on(b, parity, abort);

@@ -182,8 +182,8 @@ fp4idx_status fp4idx_rope_qk(const void* q, int64_t q_token_stride, int64_t q_he
  *   q_starts      int32 [batch+1], ascending within [0, q_tokens].  Rows of out
  *                 and lse in no sequence are left as they were.
  *   k_starts      int32 [batch+1], ascending within [0, k_tokens], or NULL.
- *   max_q         a bound on n_b; tokens of a sequence behind its max_q-th are
- *                 left unwritten.
+ *   max_q         a bound on n_b, at least 1; tokens of a sequence behind its
+ *                 max_q-th are left unwritten.
  *   max_k         a bound on c_b; keys behind a sequence's max_k-th are not
  *                 seen.  The work split is chosen by both bounds, so loose ones
  *                 cost time, not correctness.
@@ -194,7 +194,8 @@ fp4idx_status fp4idx_rope_qk(const void* q, int64_t q_token_stride, int64_t q_he
  *                 logarithm.  Neither lies in the memory of an input (out where q,
  *                 k or v begins: FP4IDX_ERR_ARG).
  *   workspace     fp4idx_prompt_workspace_bytes(batch, max_q, num_heads,
- *                 kv_heads, head_dim) bytes (0 bytes: arguments out of range),
+ *                 kv_heads, head_dim) bytes (0 bytes: arguments out of range;
+ *                 20 MB for heads of 64, 40 MB for heads of 128, whatever the rest),
  *                 16-byte aligned, contents not kept; its own for each call in
  *                 flight (two captured graphs that may run at once too).
  *                 Fewer bytes return FP4IDX_ERR_SCRATCH.
