@@ -129,7 +129,7 @@ struct Item {
   int nt;         // tiles in all, at least one
 };
 
-// The rows' chunk rc of sequence b; false: it has no rows.
+// The rows' chunk rc of sequence b; false: it has no rows, nor has any behind it.
 __device__ __forceinline__ bool item_of(const PromptArgs& a, int b, int rc, Item& m) {
   m.q0 = min(max(__ldg(a.q_starts + b), 0), a.Tq);
   const int n = min(max(__ldg(a.q_starts + b + 1), m.q0), a.Tq) - m.q0;
@@ -206,12 +206,17 @@ __device__ __forceinline__ void locate_share(const PromptArgs& a, Share& sh) {
   int64_t own = 0;
   int items = 0;
   Item m;
-  for (int64_t p = p0, b = b0, rc = rc0; p < p1; ++p) {
+  for (int64_t p = p0, b = b0, rc = rc0; p < p1;) {
     if (item_of(a, (int)b, (int)rc, m)) {
       own += m.nt + kStart;
       ++items;
+      ++p;
+      ++rc;
+    } else {  // (a call may have thousands of sequences, few as long as the longest)
+      p += a.rc_max - rc;
+      rc = a.rc_max;
     }
-    if (++rc == a.rc_max) {
+    if (rc == a.rc_max) {
       rc = 0;
       ++b;
     }
@@ -262,8 +267,11 @@ __device__ __forceinline__ void locate_share(const PromptArgs& a, Share& sh) {
           break;
         }
         at += u;
+        ++rc;
+      } else {
+        rc = a.rc_max;
       }
-      if (++rc == a.rc_max) {
+      if (rc == a.rc_max) {
         rc = 0;
         ++b;
       }
@@ -846,12 +854,16 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(const __grid_consta
       if (++head < a.Hkv) return;
       head = 0;
       Item it;
-      do {
-        if (++rc == a.rc_max) {
-          rc = 0;
-          ++b;
-        }
-      } while (!item_of(a, b, rc, it));
+      if (++rc < a.rc_max && item_of(a, b, rc, it)) return;
+      // the next sequence with rows, 32 looked at at once: the other warps' waits for
+      // the next segment run out after a second
+      rc = 0;
+      for (++b;; b += 32) {
+        const uint32_t has =
+            __ballot_sync(kFull, lane < a.batch - b && item_of(a, b + lane, 0, it));
+        if (has != 0) b += __ffs(has) - 1;
+        if (has != 0 || a.batch - b <= 32) break;
+      }
     };
     if (theirs) {
       at += share.units;
